@@ -383,6 +383,36 @@ moe_status_t moe_qk_rmsnorm(moe_bf16_t* q, moe_bf16_t* k, int64_t T, int num_q_h
                             const moe_bf16_t* k_weight, float weight_bias, float eps,
                             moe_stream_t stream);
 
+/*
+ * RMS norm of token rows with the residual's addition: the norm in front of
+ * the router and the experts. The pages have no counterpart; the formula is
+ * that of moe_qk_rmsnorm over whole rows.
+ *
+ *   h = x[t, :] + residual[t, :]   (float32; h = x[t, :] if residual is NULL)
+ *   residual_out[t, :] = bf16_rn(h)
+ *   out[t, :] = bf16_rn( (weight + weight_bias) * (h * r) ),
+ *   r = 1 / sqrt(sum(h^2) / H + eps)   (float32)
+ * The norm is taken of the float32 sum, before the residual is rounded. The
+ * sum of squares is float32: rows with |h| above about 1e19 overflow it.
+ * x, residual, out, residual_out [T, H], weight [H]: bfloat16, 16-byte
+ * aligned, H a multiple of 8. residual_out may be NULL (not stored), must be
+ * NULL if residual is, and may be residual itself (in place); apart from
+ * that outputs must not overlap inputs. eps must be >= 0
+ * (MOE_ERR_INVALID_ARG).
+ *
+ * moe_add_rmsnorm_mxfp8 stores the same rows as MXFP8 (see above: codes
+ * [T, H], 16-byte aligned, scales [T, H/32]; H a multiple of 32), quantized
+ * from the bfloat16 values of out; out may then be NULL (not stored). A
+ * router that reads out and experts that read the codes see the same rows.
+ */
+moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const moe_bf16_t* residual, int64_t T, int H,
+                             const moe_bf16_t* weight, float weight_bias, float eps,
+                             moe_bf16_t* out, moe_bf16_t* residual_out, moe_stream_t stream);
+moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residual, int64_t T, int H,
+                                   const moe_bf16_t* weight, float weight_bias, float eps,
+                                   uint8_t* codes, uint8_t* scales, moe_bf16_t* out,
+                                   moe_bf16_t* residual_out, moe_stream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -83,6 +83,11 @@ def load_library():
         lib.moe_qk_rmsnorm.argtypes = [_vp, _vp, _i64, _int, _int, _int, _vp, _vp, ctypes.c_float,
                                        ctypes.c_float, _vp]
         lib.moe_qk_rmsnorm.restype = _int
+        lib.moe_add_rmsnorm.argtypes = [_vp, _vp, _i64, _int, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]
+        lib.moe_add_rmsnorm.restype = _int
+        lib.moe_add_rmsnorm_mxfp8.argtypes = [_vp, _vp, _i64, _int, _vp, ctypes.c_float, ctypes.c_float,
+                                              _vp, _vp, _vp, _vp, _vp]
+        lib.moe_add_rmsnorm_mxfp8.restype = _int
         lib.moe_expand.argtypes = [_vp, _i64, _int, _int, _vp, _vp, _vp]
         lib.moe_expand.restype = _int
         lib.moe_swiglu.argtypes = [_vp, _i64, _int, _vp, _vp]
@@ -497,3 +502,89 @@ def moe_qk_rmsnorm(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_w
                                                            _ptr(k_weight), float(weight_bias), float(eps),
                                                            _stream_ptr(stream, q.device)))
     return q, k
+
+
+# ---------------------------------------------------------------------------
+# RMS norm of token rows with the residual's addition
+# ---------------------------------------------------------------------------
+
+def _same_device(dev: torch.device, **tensors):
+    """The kernels run on ``dev``, which must be the current device: a launch
+    on another one would read these pointers where they do not exist."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _outlive(stream: Optional[torch.cuda.Stream], *tensors):
+    """Memory this module allocated on the current stream for work on another
+    one must not be handed out again before that work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _norm_args(x, residual, weight, out, residual_out):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _need(x, "x", torch.bfloat16, (T, H))
+    _need(weight, "weight", torch.bfloat16, (H,))
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, H))
+        if residual_out is None:
+            residual_out = residual
+        _need(residual_out, "residual_out", torch.bfloat16, (T, H))
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    _same_device(x.device, residual=residual, weight=weight, out=out, residual_out=residual_out)
+    return T, H, residual_out
+
+
+def moe_add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor,
+                    weight_bias: float = 0.0, eps: float = 1e-6, *, out: Optional[torch.Tensor] = None,
+                    residual_out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """``h = x + residual`` and its RMS norm ``(w + weight_bias) * h *
+    rsqrt(mean(h^2) + eps)`` over rows of ``x [T, H]`` (bfloat16). The sum is
+    written to ``residual_out`` (default: ``residual``, in place). Returns
+    ``(out, residual_out)``; without a residual the norm of x and None."""
+    T, H, residual_out = _norm_args(x, residual, weight, out, residual_out)
+    if out is None:
+        out = torch.empty_like(x)
+        _outlive(stream, out)
+    _need(out, "out", torch.bfloat16, (T, H))
+    _check("moe_add_rmsnorm", load_library().moe_add_rmsnorm(
+        _ptr(x), _ptr(residual), T, H, _ptr(weight), float(weight_bias), float(eps), _ptr(out), _ptr(residual_out),
+        _stream_ptr(stream, x.device)))
+    return out, residual_out
+
+
+def moe_add_rmsnorm_mxfp8(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor,
+                          weight_bias: float = 0.0, eps: float = 1e-6, *, codes: Optional[torch.Tensor] = None,
+                          scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          residual_out: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None):
+    """``moe_add_rmsnorm`` with its rows stored as MXFP8: returns ``(codes
+    uint8 [T, H], scales uint8 [T, H/32], residual_out)``. Pass ``out`` to
+    have the bfloat16 rows stored too."""
+    T, H, residual_out = _norm_args(x, residual, weight, out, residual_out)
+    dev = x.device
+    if codes is None:
+        codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
+        _outlive(stream, codes)
+    if scales is None:
+        scales = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
+        _outlive(stream, scales)
+    _need(codes, "codes", torch.uint8, (T, H))
+    _need(scales, "scales", torch.uint8, (T, H // 32))
+    if out is not None:
+        _need(out, "out", torch.bfloat16, (T, H))
+    _same_device(dev, codes=codes, scales=scales)
+    _check("moe_add_rmsnorm_mxfp8", load_library().moe_add_rmsnorm_mxfp8(
+        _ptr(x), _ptr(residual), T, H, _ptr(weight), float(weight_bias), float(eps), _ptr(codes), _ptr(scales),
+        _ptr(out), _ptr(residual_out), _stream_ptr(stream, dev)))
+    return codes, scales, residual_out

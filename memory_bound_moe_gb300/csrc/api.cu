@@ -499,4 +499,53 @@ moe_status_t moe_qk_rmsnorm(moe_bf16_t* q, moe_bf16_t* k, int64_t T, int num_q_h
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// Common rules of the two norm calls. codes == NULL in the bfloat16 form.
+moe_status_t add_rmsnorm(const moe_bf16_t* x, const moe_bf16_t* residual, int64_t T, int H,
+                         const moe_bf16_t* weight, float weight_bias, float eps, moe_bf16_t* out,
+                         moe_bf16_t* residual_out, uint8_t* codes, uint8_t* scales,
+                         moe_stream_t stream) {
+    if (residual == nullptr && residual_out != nullptr) return MOE_ERR_INVALID_ARG;
+    if ((residual != nullptr && !aligned16(residual)) || (out != nullptr && !aligned16(out)) ||
+        (residual_out != nullptr && !aligned16(residual_out)) || !aligned16(x) || !aligned16(weight) ||
+        (codes != nullptr && !aligned16(codes)))
+        return MOE_ERR_MISALIGNED;
+    const uint64_t n = uint64_t(T) * uint64_t(H);
+    const Range in_x{x, 2 * n}, in_w{weight, 2ull * H}, in_r{residual, residual != nullptr ? 2 * n : 0};
+    const Range o_y{out, out != nullptr ? 2 * n : 0}, o_r{residual_out, residual_out != nullptr ? 2 * n : 0};
+    const Range o_c{codes, codes != nullptr ? n : 0}, o_s{scales, codes != nullptr ? n / 32 : 0};
+    if (any_overlap({o_y, o_r, o_c, o_s}, {in_x, in_w})) return MOE_ERR_INVALID_ARG;
+    if (any_overlap({o_y, o_c, o_s}, {in_r})) return MOE_ERR_INVALID_ARG;
+    if (residual_out != residual && overlap(o_r, in_r)) return MOE_ERR_INVALID_ARG;   // in place, or apart
+    return from_cuda(moe::launch_add_rmsnorm(x, residual, T, H, weight, weight_bias, eps, out, residual_out,
+                                             codes, scales, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const moe_bf16_t* residual, int64_t T, int H,
+                             const moe_bf16_t* weight, float weight_bias, float eps, moe_bf16_t* out,
+                             moe_bf16_t* residual_out, moe_stream_t stream) {
+    const moe_status_t st = check_rows(T, H, 1);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (x == nullptr || weight == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+    return add_rmsnorm(x, residual, T, H, weight, weight_bias, eps, out, residual_out, nullptr, nullptr, stream);
+}
+
+moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residual, int64_t T, int H,
+                                   const moe_bf16_t* weight, float weight_bias, float eps,
+                                   uint8_t* codes, uint8_t* scales, moe_bf16_t* out,
+                                   moe_bf16_t* residual_out, moe_stream_t stream) {
+    const moe_status_t st = check_rows(T, H, 1);
+    if (st != MOE_OK) return st;
+    if (H % 32 != 0) return MOE_ERR_MISALIGNED;
+    if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (x == nullptr || weight == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
+    return add_rmsnorm(x, residual, T, H, weight, weight_bias, eps, out, residual_out, codes, scales, stream);
+}
+
 }  // extern "C"

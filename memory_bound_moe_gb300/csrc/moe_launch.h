@@ -80,4 +80,11 @@ cudaError_t launch_qk_rmsnorm(uint16_t* q, uint16_t* k, int64_t T, int nq, int n
                               const uint16_t* qw, const uint16_t* kw, float bias, float eps,
                               int num_sms, cudaStream_t stream);
 
+// RMS norm of rows with the residual's addition (rmsnorm.cu): residual,
+// out and residual_out may be NULL; codes != NULL adds the MXFP8 output.
+cudaError_t launch_add_rmsnorm(const uint16_t* x, const uint16_t* residual, int64_t T, int H,
+                               const uint16_t* weight, float bias, float eps, uint16_t* out,
+                               uint16_t* residual_out, uint8_t* codes, uint8_t* scales,
+                               cudaStream_t stream);
+
 }  // namespace moe
