@@ -413,6 +413,66 @@ moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residu
                                    uint8_t* codes, uint8_t* scales, moe_bf16_t* out,
                                    moe_bf16_t* residual_out, moe_stream_t stream);
 
+/*
+ * Products of a few tokens with a 4-bit weight matrix, for the dense
+ * projections of a decode step.
+ *
+ *   y[t, n] = sum_k x[t, k] * W[n, k]   (float32 sums)
+ * x [T, K] bfloat16; W in the formats of moe_swiglu_fp4 (`format`,
+ * global_scale): codes [N, K/2], scales [N, K/32] (MXFP4) or [N, K/16]
+ * (NVFP4), row-major. y [T, N], bfloat16 (rounded once) or, with y_float32
+ * != 0, float32 (logits). The weights' values are exact; a scale byte that
+ * encodes NaN makes its block NaN.
+ * T <= MOE_FEW_MAX_TOKENS and K <= 2^20 (MOE_ERR_UNSUPPORTED); K a multiple
+ * of 32, x, codes and scales 16-byte, y 4-byte aligned (MOE_ERR_MISALIGNED);
+ * N any positive number. Results do not depend on timing; needs no workspace.
+ */
+#define MOE_FEW_MAX_TOKENS 32
+moe_status_t moe_gemv_fp4(const moe_bf16_t* x, int64_t T, int K, const uint8_t* codes,
+                          const uint8_t* scales, int N, int format, float global_scale, void* y,
+                          int y_float32, moe_stream_t stream);
+
+/*
+ * A whole MoE layer for a few tokens, in two kernels: routing, the experts'
+ * products and the weighted combine.
+ * "CuTeDSL at Perplexity", section "Prefill and decode specialization", has
+ * decode kernels of their own; the pages leave the experts' products to
+ * GEMM libraries.
+ *
+ *   ids, w     = the top-k experts and weights of moe_route(logits, renorm)
+ *   a[t, j, :] = bf16_rn( w[t, j] * silu(W13[e, 0..I) x_t) * (W13[e, I..2I) x_t) )
+ *   out[t, :]  = bf16_rn( sum_j W2[e] a[t, j, :] ),   e = ids[t, j]
+ * with float32 products, sums and silu (the weight enters before a's one
+ * rounding; a stays in the workspace). logits [T, E] float32, x [T, H],
+ * w13 [E, 2I, H] (gate rows first), w2 [E, H, I], out [T, H], bfloat16.
+ * topk_ids [T, k] and topk_weights [T, k] get the routing of moe_route, bit
+ * for bit; either may be NULL.
+ *
+ * moe_layer_fp4 takes 4-bit weights in the formats of moe_swiglu_fp4: codes
+ * [E, 2I, H/2] and [E, H, I/2], scales [E, 2I, H/b] and [E, H, I/b] with
+ * b = 32 (MXFP4) or 16 (NVFP4), and for NVFP4 one float32 tensor scale per
+ * expert and matrix in device memory, w13_global [E] and w2_global [E] (finite
+ * and positive; NULL for MXFP4).
+ *
+ * Weights of experts that no token chose are not read. Logits are assumed
+ * finite (others: unspecified, in-bounds picks). Limits: T <=
+ * MOE_FEW_MAX_TOKENS, H and I <= 2^20 (MOE_ERR_UNSUPPORTED) and multiples of
+ * 8, of 32 for 4-bit weights (MOE_ERR_MISALIGNED); all weights and scales
+ * 16-byte aligned. workspace: moe_layer_workspace_size(T, E, k, H, I) bytes,
+ * 16-byte aligned; contents need no preparation. Calls that share one must be
+ * ordered, and so must graphs that captured it.
+ */
+moe_status_t moe_layer_workspace_size(int64_t T, int E, int k, int H, int I, size_t* bytes);
+moe_status_t moe_layer(const float* logits, int64_t T, int E, int k, int renorm, const moe_bf16_t* x, int H,
+                       int I, const moe_bf16_t* w13, const moe_bf16_t* w2, moe_bf16_t* out,
+                       int32_t* topk_ids, float* topk_weights, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream);
+moe_status_t moe_layer_fp4(const float* logits, int64_t T, int E, int k, int renorm, const moe_bf16_t* x, int H,
+                           int I, int format, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                           const float* w13_global, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                           const float* w2_global, moe_bf16_t* out, int32_t* topk_ids, float* topk_weights,
+                           void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -88,6 +88,16 @@ def load_library():
         lib.moe_add_rmsnorm_mxfp8.argtypes = [_vp, _vp, _i64, _int, _vp, ctypes.c_float, ctypes.c_float,
                                               _vp, _vp, _vp, _vp, _vp]
         lib.moe_add_rmsnorm_mxfp8.restype = _int
+        lib.moe_gemv_fp4.argtypes = [_vp, _i64, _int, _vp, _vp, _int, _int, ctypes.c_float, _vp, _int, _vp]
+        lib.moe_gemv_fp4.restype = _int
+        lib.moe_layer_workspace_size.argtypes = [_i64, _int, _int, _int, _int, ctypes.POINTER(ctypes.c_size_t)]
+        lib.moe_layer_workspace_size.restype = _int
+        lib.moe_layer.argtypes = [_vp, _i64, _int, _int, _int, _vp, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  ctypes.c_size_t, _vp]
+        lib.moe_layer.restype = _int
+        lib.moe_layer_fp4.argtypes = [_vp, _i64, _int, _int, _int, _vp, _int, _int, _int, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        lib.moe_layer_fp4.restype = _int
         lib.moe_expand.argtypes = [_vp, _i64, _int, _int, _vp, _vp, _vp]
         lib.moe_expand.restype = _int
         lib.moe_swiglu.argtypes = [_vp, _i64, _int, _vp, _vp]
@@ -588,3 +598,130 @@ def moe_add_rmsnorm_mxfp8(x: torch.Tensor, residual: Optional[torch.Tensor], wei
         _ptr(x), _ptr(residual), T, H, _ptr(weight), float(weight_bias), float(eps), _ptr(codes), _ptr(scales),
         _ptr(out), _ptr(residual_out), _stream_ptr(stream, dev)))
     return codes, scales, residual_out
+
+
+# ---------------------------------------------------------------------------
+# Products for a few tokens: 4-bit weights, and whole MoE layers
+# ---------------------------------------------------------------------------
+
+def moe_gemv_fp4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: str = "nvfp4",
+                 global_scale: float = 1.0, *, out: Optional[torch.Tensor] = None,
+                 out_dtype: torch.dtype = torch.bfloat16,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``x [T, K] @ W.T`` for up to 32 tokens (bfloat16) and a 4-bit weight
+    matrix: ``codes`` uint8 [N, K/2], ``scales`` uint8 [N, K/16] (NVFP4, with
+    the tensor scale ``global_scale``) or [N, K/32] (MXFP4). Returns [T, N] in
+    ``out_dtype`` (bfloat16 or float32)."""
+    code, block = _fp4(fmt)
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x must be [T, K] and codes [N, K/2]")
+    T, K = x.shape
+    N = codes.shape[0]
+    _need(x, "x", torch.bfloat16, (T, K))
+    _need(codes, "codes", torch.uint8, (N, K // 2))
+    _need(scales, "scales", torch.uint8, (N, K // block))
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out: dtype {out_dtype}, expected torch.bfloat16 or torch.float32")
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=dev)
+        _outlive(stream, out)
+    _need(out, "out", out_dtype, (T, N))
+    _same_device(dev, codes=codes, scales=scales, out=out)
+    _check("moe_gemv_fp4", load_library().moe_gemv_fp4(
+        _ptr(x), T, K, _ptr(codes), _ptr(scales), N, code, float(global_scale), _ptr(out),
+        int(out_dtype == torch.float32), _stream_ptr(stream, dev)))
+    return out
+
+
+def moe_layer_workspace_size(T: int, E: int, k: int, H: int, I: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_layer_workspace_size",
+           load_library().moe_layer_workspace_size(int(T), int(E), int(k), int(H), int(I), ctypes.byref(out)))
+    return out.value
+
+
+def _layer_buffers(logits, x, k, out, topk_ids, topk_weights, workspace, stream, I, **weights):
+    """Checks shared by the layer calls; returns the allocated (out, workspace)."""
+    T, E = logits.shape
+    H = x.shape[1]
+    dev = x.device
+    _need(logits, "logits", torch.float32, (T, E))
+    _need(x, "x", torch.bfloat16, (T, H))
+    need = moe_layer_workspace_size(T, E, k, H, I)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        _outlive(stream, out)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        _outlive(stream, workspace)
+    _need(out, "out", torch.bfloat16, (T, H))
+    if topk_ids is not None:
+        _need(topk_ids, "topk_ids", torch.int32, (T, k))
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, (T, k))
+    _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    _same_device(dev, logits=logits, out=out, topk_ids=topk_ids, topk_weights=topk_weights, workspace=workspace,
+                 **weights)
+    return out, workspace
+
+
+def moe_layer(logits: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, k: int, renorm: bool, *,
+              out: Optional[torch.Tensor] = None, topk_ids: Optional[torch.Tensor] = None,
+              topk_weights: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """A whole MoE layer for up to 32 tokens: routing of ``logits [T, E]``,
+    the chosen experts' gated products of ``x [T, H]`` with ``w13 [E, 2I, H]``
+    (gate rows first) and ``w2 [E, H, I]`` (bfloat16), and the weighted
+    combine. Returns ``out [T, H]``; ``topk_ids`` / ``topk_weights`` [T, k],
+    when given, get the routing. ``workspace``: a uint8 tensor of
+    ``moe_layer_workspace_size(T, E, k, H, I)`` bytes (allocated when
+    omitted)."""
+    if logits.dim() != 2 or x.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("logits must be [T, E], x [T, H], w13 [E, 2I, H] and w2 [E, H, I]")
+    T, E = logits.shape
+    H, I = x.shape[1], w2.shape[2]
+    _need(w13, "w13", torch.bfloat16, (E, 2 * I, H))
+    _need(w2, "w2", torch.bfloat16, (E, H, I))
+    out, workspace = _layer_buffers(logits, x, k, out, topk_ids, topk_weights, workspace, stream, I, w13=w13, w2=w2)
+    _check("moe_layer", load_library().moe_layer(
+        _ptr(logits), T, E, int(k), int(bool(renorm)), _ptr(x), H, I, _ptr(w13), _ptr(w2), _ptr(out), _ptr(topk_ids),
+        _ptr(topk_weights), _ptr(workspace), workspace.numel(), _stream_ptr(stream, x.device)))
+    return out
+
+
+def moe_layer_fp4(logits: torch.Tensor, x: torch.Tensor, w13_codes: torch.Tensor, w13_scales: torch.Tensor,
+                  w2_codes: torch.Tensor, w2_scales: torch.Tensor, k: int, renorm: bool, fmt: str = "nvfp4",
+                  w13_global: Optional[torch.Tensor] = None, w2_global: Optional[torch.Tensor] = None, *,
+                  out: Optional[torch.Tensor] = None, topk_ids: Optional[torch.Tensor] = None,
+                  topk_weights: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``moe_layer`` with 4-bit weights: codes uint8 [E, 2I, H/2] and
+    [E, H, I/2], scales uint8 with a value per 16 (NVFP4) or 32 (MXFP4)
+    weights, and for NVFP4 the experts' tensor scales, float32 [E]."""
+    code, block = _fp4(fmt)
+    if logits.dim() != 2 or x.dim() != 2 or w13_codes.dim() != 3 or w2_codes.dim() != 3:
+        raise ValueError("logits must be [T, E], x [T, H], w13_codes [E, 2I, H/2] and w2_codes [E, H, I/2]")
+    T, E = logits.shape
+    H, I = x.shape[1], w2_codes.shape[2] * 2
+    _need(w13_codes, "w13_codes", torch.uint8, (E, 2 * I, H // 2))
+    _need(w13_scales, "w13_scales", torch.uint8, (E, 2 * I, H // block))
+    _need(w2_codes, "w2_codes", torch.uint8, (E, H, I // 2))
+    _need(w2_scales, "w2_scales", torch.uint8, (E, H, I // block))
+    if fmt == "nvfp4":
+        if w13_global is None or w2_global is None:
+            raise ValueError("NVFP4 weights need w13_global and w2_global")
+        _need(w13_global, "w13_global", torch.float32, (E,))
+        _need(w2_global, "w2_global", torch.float32, (E,))
+    elif w13_global is not None or w2_global is not None:
+        raise ValueError("MXFP4 weights have no tensor scales")
+    out, workspace = _layer_buffers(logits, x, k, out, topk_ids, topk_weights, workspace, stream, I,
+                                    w13_codes=w13_codes, w13_scales=w13_scales, w2_codes=w2_codes,
+                                    w2_scales=w2_scales, w13_global=w13_global, w2_global=w2_global)
+    _check("moe_layer_fp4", load_library().moe_layer_fp4(
+        _ptr(logits), T, E, int(k), int(bool(renorm)), _ptr(x), H, I, code, _ptr(w13_codes), _ptr(w13_scales),
+        _ptr(w13_global), _ptr(w2_codes), _ptr(w2_scales), _ptr(w2_global), _ptr(out), _ptr(topk_ids),
+        _ptr(topk_weights), _ptr(workspace), workspace.numel(), _stream_ptr(stream, x.device)))
+    return out

@@ -548,4 +548,137 @@ moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residu
     return add_rmsnorm(x, residual, T, H, weight, weight_bias, eps, out, residual_out, codes, scales, stream);
 }
 
+namespace {
+
+// Sizes of the products for a few tokens: T <= MOE_FEW_MAX_TOKENS, widths up
+// to 2^20 (32-bit offsets inside a row).
+moe_status_t check_few(int64_t T, int64_t width) {
+    if (T < 0 || width < 1) return MOE_ERR_INVALID_ARG;
+    if (T > MOE_FEW_MAX_TOKENS || width > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+uint64_t fp4_scales(uint64_t values, int format) { return values / (format == MOE_FP4_NVFP4 ? 16 : 32); }
+
+}  // namespace
+
+moe_status_t moe_gemv_fp4(const moe_bf16_t* x, int64_t T, int K, const uint8_t* codes,
+                          const uint8_t* scales, int N, int format, float global_scale, void* y,
+                          int y_float32, moe_stream_t stream) {
+    moe_status_t st = check_few(T, K);
+    if (st != MOE_OK) return st;
+    if (N < 1) return MOE_ERR_INVALID_ARG;
+    if ((st = check_fp4(format, K, global_scale)) != MOE_OK) return st;
+    if (K % 32 != 0) return MOE_ERR_MISALIGNED;   // a row of codes is whole 16-byte vectors
+    if (T == 0) return MOE_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned4(y)) return MOE_ERR_MISALIGNED;
+    const uint64_t n = uint64_t(N) * uint64_t(K);
+    if (any_overlap({{y, (y_float32 ? 4ull : 2ull) * uint64_t(T) * uint64_t(N)}},
+                    {{x, 2 * uint64_t(T) * uint64_t(K)}, {codes, n / 2}, {scales, fp4_scales(n, format)}}))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if (current_sm_count(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return from_cuda(moe::launch_gemv_fp4(x, int(T), K, codes, scales, N, format == MOE_FP4_NVFP4, global_scale, y,
+                                          y_float32 != 0, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+moe_status_t check_layer_sizes(int64_t T, int E, int k, int H, int I) {
+    moe_status_t st = check_route_sizes(T, E, k);
+    if (st != MOE_OK) return st;
+    if ((st = check_few(T, H)) != MOE_OK) return st;
+    if ((st = check_few(T, I)) != MOE_OK) return st;
+    if (H % 8 != 0 || I % 8 != 0) return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+// Everything of a layer call but its weights; `weights` are their ranges.
+moe_status_t run_layer(moe::LayerArgs& a, moe::LayerFormat format, const float* logits, int64_t T, int E, int k,
+                       int renorm, const moe_bf16_t* x, int H, int I, moe_bf16_t* out, int32_t* topk_ids,
+                       float* topk_weights, void* workspace, size_t workspace_bytes, moe_stream_t stream,
+                       std::initializer_list<Range> weights) {
+    if (logits == nullptr || x == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(logits) || !aligned16(x) || !aligned16(out) || (topk_ids != nullptr && !aligned4(topk_ids)) ||
+        (topk_weights != nullptr && !aligned4(topk_weights)))
+        return MOE_ERR_MISALIGNED;
+    const uint64_t S = uint64_t(T) * uint64_t(k), need = 2 * S * uint64_t(I);
+    if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOE_ERR_MISALIGNED;
+    const Range o_out{out, 2 * uint64_t(T) * H}, o_id{topk_ids, topk_ids != nullptr ? 4 * S : 0},
+        o_w{topk_weights, topk_weights != nullptr ? 4 * S : 0}, o_ws{workspace, need};
+    if (any_overlap({o_out, o_id, o_w, o_ws}, {{logits, 4ull * uint64_t(T) * E}, {x, 2 * uint64_t(T) * H}}) ||
+        any_overlap({o_out, o_id, o_w, o_ws}, weights))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if (current_sm_count(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+    a.logits = logits;
+    a.x = x;
+    a.out = out;
+    a.topk_ids = topk_ids;
+    a.topk_weights = topk_weights;
+    a.act = static_cast<uint16_t*>(workspace);
+    a.T = int(T); a.E = E; a.k = k; a.renorm = renorm ? 1 : 0; a.H = H; a.I = I;
+    return from_cuda(moe::launch_layer(a, format, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+moe_status_t moe_layer_workspace_size(int64_t T, int E, int k, int H, int I, size_t* bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    const moe_status_t st = check_layer_sizes(T, E, k, H, I);
+    if (st != MOE_OK) return st;
+    *bytes = 2 * size_t(T) * size_t(k) * size_t(I);   // the activation, bfloat16
+    return MOE_OK;
+}
+
+moe_status_t moe_layer(const float* logits, int64_t T, int E, int k, int renorm, const moe_bf16_t* x, int H,
+                       int I, const moe_bf16_t* w13, const moe_bf16_t* w2, moe_bf16_t* out,
+                       int32_t* topk_ids, float* topk_weights, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream) {
+    const moe_status_t st = check_layer_sizes(T, E, k, H, I);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (w13 == nullptr || w2 == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(w13) || !aligned16(w2)) return MOE_ERR_MISALIGNED;
+    const uint64_t n = uint64_t(E) * uint64_t(H) * uint64_t(I);
+    moe::LayerArgs a = {};
+    a.w13 = w13;
+    a.w2 = w2;
+    return run_layer(a, moe::kLayerBf16, logits, T, E, k, renorm, x, H, I, out, topk_ids, topk_weights, workspace,
+                     workspace_bytes, stream, {{w13, 4 * n}, {w2, 2 * n}});
+}
+
+moe_status_t moe_layer_fp4(const float* logits, int64_t T, int E, int k, int renorm, const moe_bf16_t* x, int H,
+                           int I, int format, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                           const float* w13_global, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                           const float* w2_global, moe_bf16_t* out, int32_t* topk_ids, float* topk_weights,
+                           void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    const moe_status_t st = check_layer_sizes(T, E, k, H, I);
+    if (st != MOE_OK) return st;
+    if (format != MOE_FP4_NVFP4 && format != MOE_FP4_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (H % 32 != 0 || I % 32 != 0) return MOE_ERR_MISALIGNED;
+    if (T == 0) return MOE_OK;
+    if (w13_codes == nullptr || w13_scales == nullptr || w2_codes == nullptr || w2_scales == nullptr)
+        return MOE_ERR_INVALID_ARG;
+    const bool nv = format == MOE_FP4_NVFP4;
+    if (nv && (w13_global == nullptr || w2_global == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(w13_codes) || !aligned16(w13_scales) || !aligned16(w2_codes) || !aligned16(w2_scales) ||
+        (nv && (!aligned4(w13_global) || !aligned4(w2_global))))
+        return MOE_ERR_MISALIGNED;
+    const uint64_t n = uint64_t(E) * uint64_t(H) * uint64_t(I), gb = nv ? 4ull * E : 0;
+    moe::LayerArgs a = {};
+    a.w13 = w13_codes;
+    a.w2 = w2_codes;
+    a.w13_scales = w13_scales;
+    a.w2_scales = w2_scales;
+    a.w13_global = w13_global;
+    a.w2_global = w2_global;
+    return run_layer(a, nv ? moe::kLayerNvfp4 : moe::kLayerMxfp4, logits, T, E, k, renorm, x, H, I, out, topk_ids,
+                     topk_weights, workspace, workspace_bytes, stream,
+                     {{w13_codes, n}, {w13_scales, fp4_scales(2 * n, format)}, {w2_codes, n / 2},
+                      {w2_scales, fp4_scales(n, format)}, {w13_global, gb}, {w2_global, gb}});
+}
+
 }  // extern "C"

@@ -87,4 +87,29 @@ cudaError_t launch_add_rmsnorm(const uint16_t* x, const uint16_t* residual, int6
                                uint16_t* residual_out, uint8_t* codes, uint8_t* scales,
                                cudaStream_t stream);
 
+// Products of T <= 32 tokens x [T, K] with 4-bit weights [N, K] (gemv_fp4.cu).
+cudaError_t launch_gemv_fp4(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales,
+                            int N, bool nvfp4, float g, void* y, bool y_f32, int num_sms,
+                            cudaStream_t stream);
+
+// A whole MoE layer for T <= 32 tokens (layer.cu). Weights: bfloat16 (w13,
+// w2), or codes with scales and, for NVFP4, a tensor scale per expert.
+struct LayerArgs {
+    const float* logits;
+    const uint16_t* x;
+    const void* w13;
+    const void* w2;
+    const uint8_t* w13_scales;   // 4-bit weights only
+    const uint8_t* w2_scales;
+    const float* w13_global;     // NVFP4 only, [E]
+    const float* w2_global;
+    uint16_t* out;
+    int32_t* topk_ids;           // may be NULL
+    float* topk_weights;         // may be NULL
+    uint16_t* act;               // workspace [T*k, I]
+    int T, E, k, renorm, H, I;
+};
+enum LayerFormat { kLayerBf16 = 0, kLayerNvfp4 = 1, kLayerMxfp4 = 2 };
+cudaError_t launch_layer(const LayerArgs& a, LayerFormat format, int num_sms, cudaStream_t stream);
+
 }  // namespace moe
