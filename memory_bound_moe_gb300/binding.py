@@ -114,8 +114,10 @@ def _check(fn: str, status: int):
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without building a Stream object (2 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
@@ -518,40 +520,63 @@ def moe_qk_rmsnorm(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_w
 # RMS norm of token rows with the residual's addition
 # ---------------------------------------------------------------------------
 
-def _same_device(dev: torch.device, **tensors):
-    """The kernels run on ``dev``, which must be the current device: a launch
-    on another one would read these pointers where they do not exist."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _device(x: torch.Tensor) -> int:
+    """The index of x's device, which must be the current one: a launch on
+    another device would read x where it does not exist."""
+    d = x.get_device()
+    if d < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    return d
 
 
-def _outlive(stream: Optional[torch.cuda.Stream], *tensors):
-    """Memory this module allocated on the current stream for work on another
-    one must not be handed out again before that work is done."""
+def _addr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The address of a tensor that is what the call needs: ``_need``, on the
+    device ``dev``. (One test for the good case: these calls take a few
+    microseconds on the GPU, so the host's checks are kept short.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    return 0 if t is None else _addr(t, name, dtype, shape, dev)
+
+
+def _new(shape: tuple, dtype: torch.dtype, x: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory on x's device for a result. It comes from the current stream's
+    pool: when the work runs on another one it must not be handed out again
+    before that work is done."""
+    t = torch.empty(shape, dtype=dtype, device=x.device)
     if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+        t.record_stream(stream)
+    return t
 
 
-def _norm_args(x, residual, weight, out, residual_out):
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    _need(x, "x", torch.bfloat16, (T, H))
-    _need(weight, "weight", torch.bfloat16, (H,))
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (T, H))
-        if residual_out is None:
-            residual_out = residual
-        _need(residual_out, "residual_out", torch.bfloat16, (T, H))
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    _same_device(x.device, residual=residual, weight=weight, out=out, residual_out=residual_out)
-    return T, H, residual_out
+def _raw_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _lib_fast():
+    return _lib if _lib is not None else load_library()
+
+
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _norm_residual(residual, residual_out, T, H, dev):
+    """(residual, residual_out, their addresses); in place by default."""
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        return None, 0, 0
+    r = _addr(residual, "residual", _bf16, (T, H), dev)
+    if residual_out is None or residual_out is residual:
+        return residual, r, r
+    return residual_out, r, _addr(residual_out, "residual_out", _bf16, (T, H), dev)
 
 
 def moe_add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor,
@@ -562,14 +587,19 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: t
     rsqrt(mean(h^2) + eps)`` over rows of ``x [T, H]`` (bfloat16). The sum is
     written to ``residual_out`` (default: ``residual``, in place). Returns
     ``(out, residual_out)``; without a residual the norm of x and None."""
-    T, H, residual_out = _norm_args(x, residual, weight, out, residual_out)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = _device(x)
+    xp = _addr(x, "x", _bf16, (T, H), dev)
+    wp = _addr(weight, "weight", _bf16, (H,), dev)
+    residual_out, rp, rop = _norm_residual(residual, residual_out, T, H, dev)
     if out is None:
-        out = torch.empty_like(x)
-        _outlive(stream, out)
-    _need(out, "out", torch.bfloat16, (T, H))
-    _check("moe_add_rmsnorm", load_library().moe_add_rmsnorm(
-        _ptr(x), _ptr(residual), T, H, _ptr(weight), float(weight_bias), float(eps), _ptr(out), _ptr(residual_out),
-        _stream_ptr(stream, x.device)))
+        out = _new((T, H), _bf16, x, stream)
+    st = _lib_fast().moe_add_rmsnorm(xp, rp, T, H, wp, weight_bias, eps, _addr(out, "out", _bf16, (T, H), dev), rop,
+                                     _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_add_rmsnorm", st)
     return out, residual_out
 
 
@@ -581,22 +611,22 @@ def moe_add_rmsnorm_mxfp8(x: torch.Tensor, residual: Optional[torch.Tensor], wei
     """``moe_add_rmsnorm`` with its rows stored as MXFP8: returns ``(codes
     uint8 [T, H], scales uint8 [T, H/32], residual_out)``. Pass ``out`` to
     have the bfloat16 rows stored too."""
-    T, H, residual_out = _norm_args(x, residual, weight, out, residual_out)
-    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = _device(x)
+    xp = _addr(x, "x", _bf16, (T, H), dev)
+    wp = _addr(weight, "weight", _bf16, (H,), dev)
+    residual_out, rp, rop = _norm_residual(residual, residual_out, T, H, dev)
     if codes is None:
-        codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
-        _outlive(stream, codes)
+        codes = _new((T, H), _u8, x, stream)
     if scales is None:
-        scales = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
-        _outlive(stream, scales)
-    _need(codes, "codes", torch.uint8, (T, H))
-    _need(scales, "scales", torch.uint8, (T, H // 32))
-    if out is not None:
-        _need(out, "out", torch.bfloat16, (T, H))
-    _same_device(dev, codes=codes, scales=scales)
-    _check("moe_add_rmsnorm_mxfp8", load_library().moe_add_rmsnorm_mxfp8(
-        _ptr(x), _ptr(residual), T, H, _ptr(weight), float(weight_bias), float(eps), _ptr(codes), _ptr(scales),
-        _ptr(out), _ptr(residual_out), _stream_ptr(stream, dev)))
+        scales = _new((T, H // 32), _u8, x, stream)
+    st = _lib_fast().moe_add_rmsnorm_mxfp8(xp, rp, T, H, wp, weight_bias, eps, _addr(codes, "codes", _u8, (T, H), dev),
+                                           _addr(scales, "scales", _u8, (T, H // 32), dev),
+                                           _opt(out, "out", _bf16, (T, H), dev), rop, _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_add_rmsnorm_mxfp8", st)
     return codes, scales, residual_out
 
 
@@ -617,22 +647,19 @@ def moe_gemv_fp4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt
         raise ValueError("x must be [T, K] and codes [N, K/2]")
     T, K = x.shape
     N = codes.shape[0]
-    _need(x, "x", torch.bfloat16, (T, K))
-    _need(codes, "codes", torch.uint8, (N, K // 2))
-    _need(scales, "scales", torch.uint8, (N, K // block))
+    dev = _device(x)
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not _bf16 and out_dtype is not _f32:
         raise TypeError(f"out: dtype {out_dtype}, expected torch.bfloat16 or torch.float32")
-    dev = x.device
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=dev)
-        _outlive(stream, out)
-    _need(out, "out", out_dtype, (T, N))
-    _same_device(dev, codes=codes, scales=scales, out=out)
-    _check("moe_gemv_fp4", load_library().moe_gemv_fp4(
-        _ptr(x), T, K, _ptr(codes), _ptr(scales), N, code, float(global_scale), _ptr(out),
-        int(out_dtype == torch.float32), _stream_ptr(stream, dev)))
+        out = _new((T, N), out_dtype, x, stream)
+    st = _lib_fast().moe_gemv_fp4(_addr(x, "x", _bf16, (T, K), dev), T, K, _addr(codes, "codes", _u8, (N, K // 2), dev),
+                                  _addr(scales, "scales", _u8, (N, K // block), dev), N, code, global_scale,
+                                  _addr(out, "out", out_dtype, (T, N), dev), out_dtype is _f32,
+                                  _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_gemv_fp4", st)
     return out
 
 
@@ -643,29 +670,11 @@ def moe_layer_workspace_size(T: int, E: int, k: int, H: int, I: int) -> int:
     return out.value
 
 
-def _layer_buffers(logits, x, k, out, topk_ids, topk_weights, workspace, stream, I, **weights):
-    """Checks shared by the layer calls; returns the allocated (out, workspace)."""
-    T, E = logits.shape
-    H = x.shape[1]
-    dev = x.device
-    _need(logits, "logits", torch.float32, (T, E))
-    _need(x, "x", torch.bfloat16, (T, H))
-    need = moe_layer_workspace_size(T, E, k, H, I)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        _outlive(stream, out)
+def _layer_workspace(workspace, T, E, k, H, I, x, dev, stream):
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _outlive(stream, workspace)
-    _need(out, "out", torch.bfloat16, (T, H))
-    if topk_ids is not None:
-        _need(topk_ids, "topk_ids", torch.int32, (T, k))
-    if topk_weights is not None:
-        _need(topk_weights, "topk_weights", torch.float32, (T, k))
-    _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    _same_device(dev, logits=logits, out=out, topk_ids=topk_ids, topk_weights=topk_weights, workspace=workspace,
-                 **weights)
-    return out, workspace
+        workspace = _new((moe_layer_workspace_size(T, E, k, H, I),), _u8, x, stream)
+    n = workspace.numel()
+    return workspace, _addr(workspace, "workspace", _u8, (n,), dev), n
 
 
 def moe_layer(logits: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, k: int, renorm: bool, *,
@@ -683,12 +692,18 @@ def moe_layer(logits: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torc
         raise ValueError("logits must be [T, E], x [T, H], w13 [E, 2I, H] and w2 [E, H, I]")
     T, E = logits.shape
     H, I = x.shape[1], w2.shape[2]
-    _need(w13, "w13", torch.bfloat16, (E, 2 * I, H))
-    _need(w2, "w2", torch.bfloat16, (E, H, I))
-    out, workspace = _layer_buffers(logits, x, k, out, topk_ids, topk_weights, workspace, stream, I, w13=w13, w2=w2)
-    _check("moe_layer", load_library().moe_layer(
-        _ptr(logits), T, E, int(k), int(bool(renorm)), _ptr(x), H, I, _ptr(w13), _ptr(w2), _ptr(out), _ptr(topk_ids),
-        _ptr(topk_weights), _ptr(workspace), workspace.numel(), _stream_ptr(stream, x.device)))
+    dev = _device(x)
+    if out is None:
+        out = _new((T, H), _bf16, x, stream)
+    workspace, ws, ws_bytes = _layer_workspace(workspace, T, E, k, H, I, x, dev, stream)
+    st = _lib_fast().moe_layer(_addr(logits, "logits", _f32, (T, E), dev), T, E, k, bool(renorm),
+                               _addr(x, "x", _bf16, (T, H), dev), H, I, _addr(w13, "w13", _bf16, (E, 2 * I, H), dev),
+                               _addr(w2, "w2", _bf16, (E, H, I), dev), _addr(out, "out", _bf16, (T, H), dev),
+                               _opt(topk_ids, "topk_ids", _i32, (T, k), dev),
+                               _opt(topk_weights, "topk_weights", _f32, (T, k), dev), ws, ws_bytes,
+                               _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_layer", st)
     return out
 
 
@@ -706,22 +721,23 @@ def moe_layer_fp4(logits: torch.Tensor, x: torch.Tensor, w13_codes: torch.Tensor
         raise ValueError("logits must be [T, E], x [T, H], w13_codes [E, 2I, H/2] and w2_codes [E, H, I/2]")
     T, E = logits.shape
     H, I = x.shape[1], w2_codes.shape[2] * 2
-    _need(w13_codes, "w13_codes", torch.uint8, (E, 2 * I, H // 2))
-    _need(w13_scales, "w13_scales", torch.uint8, (E, 2 * I, H // block))
-    _need(w2_codes, "w2_codes", torch.uint8, (E, H, I // 2))
-    _need(w2_scales, "w2_scales", torch.uint8, (E, H, I // block))
+    dev = _device(x)
     if fmt == "nvfp4":
         if w13_global is None or w2_global is None:
             raise ValueError("NVFP4 weights need w13_global and w2_global")
-        _need(w13_global, "w13_global", torch.float32, (E,))
-        _need(w2_global, "w2_global", torch.float32, (E,))
     elif w13_global is not None or w2_global is not None:
         raise ValueError("MXFP4 weights have no tensor scales")
-    out, workspace = _layer_buffers(logits, x, k, out, topk_ids, topk_weights, workspace, stream, I,
-                                    w13_codes=w13_codes, w13_scales=w13_scales, w2_codes=w2_codes,
-                                    w2_scales=w2_scales, w13_global=w13_global, w2_global=w2_global)
-    _check("moe_layer_fp4", load_library().moe_layer_fp4(
-        _ptr(logits), T, E, int(k), int(bool(renorm)), _ptr(x), H, I, code, _ptr(w13_codes), _ptr(w13_scales),
-        _ptr(w13_global), _ptr(w2_codes), _ptr(w2_scales), _ptr(w2_global), _ptr(out), _ptr(topk_ids),
-        _ptr(topk_weights), _ptr(workspace), workspace.numel(), _stream_ptr(stream, x.device)))
+    if out is None:
+        out = _new((T, H), _bf16, x, stream)
+    workspace, ws, ws_bytes = _layer_workspace(workspace, T, E, k, H, I, x, dev, stream)
+    st = _lib_fast().moe_layer_fp4(
+        _addr(logits, "logits", _f32, (T, E), dev), T, E, k, bool(renorm), _addr(x, "x", _bf16, (T, H), dev), H, I, code,
+        _addr(w13_codes, "w13_codes", _u8, (E, 2 * I, H // 2), dev),
+        _addr(w13_scales, "w13_scales", _u8, (E, 2 * I, H // block), dev), _opt(w13_global, "w13_global", _f32, (E,), dev),
+        _addr(w2_codes, "w2_codes", _u8, (E, H, I // 2), dev), _addr(w2_scales, "w2_scales", _u8, (E, H, I // block), dev),
+        _opt(w2_global, "w2_global", _f32, (E,), dev), _addr(out, "out", _bf16, (T, H), dev),
+        _opt(topk_ids, "topk_ids", _i32, (T, k), dev), _opt(topk_weights, "topk_weights", _f32, (T, k), dev), ws, ws_bytes,
+        _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_layer_fp4", st)
     return out

@@ -594,8 +594,10 @@ moe_status_t check_layer_sizes(int64_t T, int E, int k, int H, int I) {
     return MOE_OK;
 }
 
+using LayerLaunch = cudaError_t (*)(const moe::LayerArgs&, int, cudaStream_t);
+
 // Everything of a layer call but its weights; `weights` are their ranges.
-moe_status_t run_layer(moe::LayerArgs& a, moe::LayerFormat format, const float* logits, int64_t T, int E, int k,
+moe_status_t run_layer(moe::LayerArgs& a, LayerLaunch launch, const float* logits, int64_t T, int E, int k,
                        int renorm, const moe_bf16_t* x, int H, int I, moe_bf16_t* out, int32_t* topk_ids,
                        float* topk_weights, void* workspace, size_t workspace_bytes, moe_stream_t stream,
                        std::initializer_list<Range> weights) {
@@ -620,7 +622,7 @@ moe_status_t run_layer(moe::LayerArgs& a, moe::LayerFormat format, const float* 
     a.topk_weights = topk_weights;
     a.act = static_cast<uint16_t*>(workspace);
     a.T = int(T); a.E = E; a.k = k; a.renorm = renorm ? 1 : 0; a.H = H; a.I = I;
-    return from_cuda(moe::launch_layer(a, format, sms, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(launch(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -646,7 +648,7 @@ moe_status_t moe_layer(const float* logits, int64_t T, int E, int k, int renorm,
     moe::LayerArgs a = {};
     a.w13 = w13;
     a.w2 = w2;
-    return run_layer(a, moe::kLayerBf16, logits, T, E, k, renorm, x, H, I, out, topk_ids, topk_weights, workspace,
+    return run_layer(a, moe::launch_layer_bf16, logits, T, E, k, renorm, x, H, I, out, topk_ids, topk_weights, workspace,
                      workspace_bytes, stream, {{w13, 4 * n}, {w2, 2 * n}});
 }
 
@@ -675,7 +677,7 @@ moe_status_t moe_layer_fp4(const float* logits, int64_t T, int E, int k, int ren
     a.w2_scales = w2_scales;
     a.w13_global = w13_global;
     a.w2_global = w2_global;
-    return run_layer(a, nv ? moe::kLayerNvfp4 : moe::kLayerMxfp4, logits, T, E, k, renorm, x, H, I, out, topk_ids,
+    return run_layer(a, nv ? moe::launch_layer_nvfp4 : moe::launch_layer_mxfp4, logits, T, E, k, renorm, x, H, I, out, topk_ids,
                      topk_weights, workspace, workspace_bytes, stream,
                      {{w13_codes, n}, {w13_scales, fp4_scales(2 * n, format)}, {w2_codes, n / 2},
                       {w2_scales, fp4_scales(n, format)}, {w13_global, gb}, {w2_global, gb}});

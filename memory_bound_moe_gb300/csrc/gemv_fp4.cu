@@ -50,13 +50,10 @@ __global__ void __launch_bounds__(kNt, 2) gemv_kernel(GemvArgs a, uint32_t C) {
                     load_gran<F>(w[i][r], h, p, row < a.N, u * U + i, q, rb);
                 }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            BGran<F> b[NG];
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-                load_x<F>(b[n], a.x + uint64_t(n * 8 + g) * a.K, n * 8 + g < a.T, u * U + i, q, a.K);
-            mma_step<F, R, NG>(acc, w[i], b, NG);
-        }
+        for (int i = 0; i < U; ++i)
+            mma_step<F, R, NG>(acc, w[i], ~0u, 1.0f, [&](int n, BGran<F>& b) {
+                load_x<F>(b, a.x + uint64_t(n * 8 + g) * a.K, n * 8 + g < a.T, u * U + i, q, a.K);
+            });
     }
     store_partial<R, NG>(s_red + warp * kOut, acc);
     __syncthreads();
@@ -106,9 +103,10 @@ cudaError_t launch_r(GemvArgs a, int num_sms, cudaStream_t stream) {
 
 template <int F>
 cudaError_t launch_f(const GemvArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.T <= 8) return launch_r<F, 1, 1>(a, num_sms, stream);
-    if (a.T <= 16) return launch_r<F, 1, 2>(a, num_sms, stream);
-    return launch_r<F, 1, 4>(a, num_sms, stream);
+    const bool wide = a.N >= 32u * 2u * uint32_t(num_sms);
+    if (a.T <= 8) return wide ? launch_r<F, 2, 1>(a, num_sms, stream) : launch_r<F, 1, 1>(a, num_sms, stream);
+    if (a.T <= 16) return wide ? launch_r<F, 2, 2>(a, num_sms, stream) : launch_r<F, 1, 2>(a, num_sms, stream);
+    return wide ? launch_r<F, 2, 4>(a, num_sms, stream) : launch_r<F, 1, 4>(a, num_sms, stream);
 }
 
 }  // namespace

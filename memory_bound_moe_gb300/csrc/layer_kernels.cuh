@@ -1,4 +1,4 @@
-// A whole MoE layer for a few tokens (T <= 32) in two kernels: routing and
+// Kernels of a whole MoE layer for a few tokens (T <= 32) in two kernels: routing and
 // fc1 with SwiGLU, then fc2 with the weighted combine.
 //
 //   ids, w = top-k of softmax(logits)   (as moe_route)
@@ -21,6 +21,8 @@
 //   (expert, k) units of all chosen experts. B columns are the tokens
 //   themselves, zero where a token is not routed to the expert.
 // All sums are taken in a fixed order: results do not depend on timing.
+#pragma once
+
 #include "few_device.cuh"
 #include "moe_launch.h"
 #include "route_device.cuh"
@@ -154,13 +156,10 @@ __global__ void __launch_bounds__(kNt, 2) fc1_kernel(LayerArgs a) {
                         load_gran<F>(w[i][r], h, p, j < I, u * U + i, q, rb);
                     }
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                BGran<F> b[NG];
-#pragma unroll
-                for (int n = 0; n < NG; ++n)
-                    if (n < groups) load_x<F>(b[n], xrow[n], xrow[n] != nullptr, u * U + i, q, K);
-                mma_step<F, R, NG>(acc, w[i], b, groups);
-            }
+            for (int i = 0; i < U; ++i)
+                mma_step<F, R, NG>(acc, w[i], (1u << groups) - 1u, 1.0f, [&](int n, BGran<F>& b) {
+                    load_x<F>(b, xrow[n], xrow[n] != nullptr, u * U + i, q, K);
+                });
         }
         store_partial<R, NG>(s_red + warp * kOut, acc);
         __syncthreads();
@@ -198,10 +197,20 @@ __global__ void __launch_bounds__(kNt, 2) fc2_kernel(LayerArgs a, uint32_t C) {
     const uint32_t rank = blockIdx.x % C, row0 = blockIdx.x / C * (16 * R);
     const uint32_t units = ((rb + 63) / 64 + U - 1) / U;   // per expert
     const uint32_t total = uint32_t(s.nd) * units;
+    // kCompact: B columns are the expert's own tokens, 8 to a group, and its
+    // sums are added to the warp's part of s_red when the warp leaves the expert
+    constexpr bool kCompact = WInfo<F>::kFp4 && NG > 1;
+    float* s_warp = s_red + warp * kOut;
+    if constexpr (kCompact) {
+        for (int o = lane; o < kOut; o += kWarp) s_warp[o] = 0.0f;
+        __syncwarp();
+    }
     float acc[R][NG][4] = {};
-    for (uint32_t v = rank * kNw + warp; v < total; v += C * kNw) {
+    const uint32_t first = rank * kNw + warp, stride = C * kNw;
+    for (uint32_t v = first; v < total; v += stride) {
         const uint32_t d = v / units, u = v - d * units;
-        const uint32_t e = s.expert[d], tokens = s.tokens[d];
+        const uint32_t e = s.expert[d], tokens = s.tokens[d], off = s.off[d];
+        const int m = __popc(tokens);
         AGran<F> w[U][R];
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -214,40 +223,47 @@ __global__ void __launch_bounds__(kNt, 2) fc2_kernel(LayerArgs a, uint32_t C) {
                     const WRow p = {static_cast<const uint8_t*>(a.w2) + row * rb, a.w2_scales + row * rs};
                     load_gran<F>(w[i][r], h, p, j < H, u * U + i, q, rb);
                 }
-        const uint32_t off = s.off[d];
-        float part[R][NG][4] = {};   // this expert's products, before its tensor scale
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                if (((tokens >> (8 * n)) & 0xffu) == 0u) continue;   // no token of this group: warp-uniform
-                const uint32_t t = n * 8 + g;
-                const bool mine = (tokens >> t) & 1u;
-                const uint32_t row = off + __popc(tokens & ((1u << t) - 1u));
-                BGran<F> b[1];
-                load_x<F>(b[0], a.act + uint64_t(row) * K, mine, u * U + i, q, K);
-                float c[R][1][4];
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) c[r][0][z] = part[r][n][z];
-                mma_step<F, R, 1>(c, w[i], b, 1);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) part[r][n][z] = c[r][0][z];
-            }
-        }
         float scale = 1.0f;
         if constexpr (F == kWNvfp4) scale = 1.0f / a.w2_global[e];
+        uint32_t live = 0;   // groups with a token of this expert: warp-uniform
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int n = 0; n < NG; ++n)
+            live |= uint32_t(kCompact ? n * 8 < m : ((tokens >> (8 * n)) & 0xffu) != 0u) << n;
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
+        for (int i = 0; i < U; ++i)
+            mma_step<F, R, NG>(acc, w[i], live, scale, [&](int n, BGran<F>& b) {
+                const uint32_t c = n * 8 + g;   // column: the expert's c-th token, or token c
+                const bool mine = kCompact ? int(c) < m : ((tokens >> c) & 1u) != 0u;
+                const uint32_t row = off + (kCompact ? c : uint32_t(__popc(tokens & ((1u << c) - 1u))));
+                load_x<F>(b, a.act + uint64_t(row) * K, mine, u * U + i, q, K);
+            });
+        if constexpr (kCompact) {
+            if (v + stride >= total || (v + stride) / units != d) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) acc[r][n][z] = fmaf(part[r][n][z], scale, acc[r][n][z]);
+                for (int n = 0; n < NG; ++n) {
+                    if (!((live >> n) & 1u)) continue;
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int c = n * 8 + 2 * q + z;
+                        if (c < m) {
+                            float* col = s_warp + nth_token(tokens, c) * (16 * R) + g;
+#pragma unroll
+                            for (int r = 0; r < R; ++r) {
+                                col[r * 16] += acc[r][n][z];
+                                col[r * 16 + 8] += acc[r][n][z + 2];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) acc[r][n][z] = 0.0f;
+                }
+                __syncwarp();
+            }
+        }
     }
-    store_partial<R, NG>(s_red + warp * kOut, acc);
+    if constexpr (!kCompact) store_partial<R, NG>(s_warp, acc);
     __syncthreads();
     if (C > 1) {
         for (int o = threadIdx.x; o < kOut; o += kNt) {
@@ -276,7 +292,7 @@ __global__ void __launch_bounds__(kNt, 2) fc2_kernel(LayerArgs a, uint32_t C) {
 
 template <int F, int NG>
 cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-    constexpr int R = 1, U = WInfo<F>::kFp4 ? 2 : 4;
+    constexpr int R = WInfo<F>::kFp4 ? 2 : 1, U = WInfo<F>::kFp4 ? 2 : 4;
     constexpr size_t smem = sizeof(float) * kNw * 8 * NG * 16 * R;
     auto fc1 = fc1_kernel<F, R, NG, U>;
     auto fc2 = fc2_kernel<F, R, NG, U>;
@@ -292,21 +308,12 @@ cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
 }
 
 template <int F>
-cudaError_t launch_f(const LayerArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_layer_f(const LayerArgs& a, int num_sms, cudaStream_t stream) {
     if (a.T <= 8) return launch_ng<F, 1>(a, num_sms, stream);
     if (a.T <= 16) return launch_ng<F, 2>(a, num_sms, stream);
     return launch_ng<F, 4>(a, num_sms, stream);
 }
 
 }  // namespace
-
-cudaError_t launch_layer(const LayerArgs& a, LayerFormat format, int num_sms, cudaStream_t stream) {
-    switch (format) {
-        case kLayerBf16: return launch_f<kWBf16>(a, num_sms, stream);
-        case kLayerNvfp4: return launch_f<kWNvfp4>(a, num_sms, stream);
-        case kLayerMxfp4: return launch_f<kWMxfp4>(a, num_sms, stream);
-    }
-    return cudaErrorInvalidValue;
-}
 
 }  // namespace moe

@@ -92,7 +92,8 @@ cudaError_t launch_gemv_fp4(const uint16_t* x, int T, int K, const uint8_t* code
                             int N, bool nvfp4, float g, void* y, bool y_f32, int num_sms,
                             cudaStream_t stream);
 
-// A whole MoE layer for T <= 32 tokens (layer.cu). Weights: bfloat16 (w13,
+// A whole MoE layer for T <= 32 tokens (layer_kernels.cuh, one
+// translation unit per weight format). Weights: bfloat16 (w13,
 // w2), or codes with scales and, for NVFP4, a tensor scale per expert.
 struct LayerArgs {
     const float* logits;
@@ -109,7 +110,8 @@ struct LayerArgs {
     uint16_t* act;               // workspace [T*k, I]
     int T, E, k, renorm, H, I;
 };
-enum LayerFormat { kLayerBf16 = 0, kLayerNvfp4 = 1, kLayerMxfp4 = 2 };
-cudaError_t launch_layer(const LayerArgs& a, LayerFormat format, int num_sms, cudaStream_t stream);
+cudaError_t launch_layer_bf16(const LayerArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_layer_nvfp4(const LayerArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_layer_mxfp4(const LayerArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace moe
