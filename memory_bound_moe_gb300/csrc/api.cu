@@ -594,6 +594,9 @@ moe_status_t check_layer_sizes(int64_t T, int E, int k, int H, int I) {
     return MOE_OK;
 }
 
+// The activation [T k, I] in bfloat16.
+uint64_t layer_workspace(int64_t T, int k, int I) { return 2 * uint64_t(T) * uint64_t(k) * uint64_t(I); }
+
 using LayerLaunch = cudaError_t (*)(const moe::LayerArgs&, int, cudaStream_t);
 
 // Everything of a layer call but its weights; `weights` are their ranges.
@@ -605,7 +608,7 @@ moe_status_t run_layer(moe::LayerArgs& a, LayerLaunch launch, const float* logit
     if (!aligned4(logits) || !aligned16(x) || !aligned16(out) || (topk_ids != nullptr && !aligned4(topk_ids)) ||
         (topk_weights != nullptr && !aligned4(topk_weights)))
         return MOE_ERR_MISALIGNED;
-    const uint64_t S = uint64_t(T) * uint64_t(k), need = 2 * S * uint64_t(I);
+    const uint64_t S = uint64_t(T) * uint64_t(k), need = layer_workspace(T, k, I);
     if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MOE_ERR_MISALIGNED;
     const Range o_out{out, 2 * uint64_t(T) * H}, o_id{topk_ids, topk_ids != nullptr ? 4 * S : 0},
@@ -631,7 +634,7 @@ moe_status_t moe_layer_workspace_size(int64_t T, int E, int k, int H, int I, siz
     if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
     const moe_status_t st = check_layer_sizes(T, E, k, H, I);
     if (st != MOE_OK) return st;
-    *bytes = 2 * size_t(T) * size_t(k) * size_t(I);   // the activation, bfloat16
+    *bytes = T == 0 ? 0 : layer_workspace(T, k, I);
     return MOE_OK;
 }
 

@@ -10,9 +10,11 @@
 // token, and feeds them to the products without any exchange between lanes:
 //   bfloat16: 8 values per granule, 32 k per step, 2 products per 16 rows;
 //   4 bits:  32 values per granule, 128 k per step, 8 products per 16 rows (f16).
-// Nothing is staged: at a few tokens per weight the kernels are bound by the
-// weights' bytes, and registers hold as many loads in flight as a
-// shared-memory ring would.
+//
+// Each warp streams its weights through a ring of its own in shared memory:
+// a lane copies its granules in with cp.async and reads the same 16 bytes
+// back, so the ring needs no barrier, costs no registers, and D chunks (4 KB
+// each) stay in flight per warp while another is being multiplied.
 #pragma once
 
 #include "moe_device.cuh"
@@ -45,53 +47,132 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The 8 E2M1 codes of w times scale (an f16 in both halves) as f16 pairs
-// (codes 2 i, 2 i + 1). Exact: 2 significant bits times at most 4.
-__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t scale, uint32_t (&p)[4]) {
-    asm("{.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t"
-        "mul.rn.f16x2 %0, %0, %5;\n\tmul.rn.f16x2 %1, %1, %5;\n\t"
-        "mul.rn.f16x2 %2, %2, %5;\n\tmul.rn.f16x2 %3, %3, %5;}"
-        : "=&r"(p[0]), "=&r"(p[1]), "=&r"(p[2]), "=&r"(p[3])
-        : "r"(w), "r"(scale));
-}
-
-// One lane's granules of two weight rows at one step, with their scales.
-template <int F>
+// One lane's granules of two weight rows (g and g + 8 of a tile) at one step.
 struct AGran {
     Bits<16> w[2];
-    uint32_t s[WInfo<F>::kFp4 ? 2 : 1];
 };
 
-// A row of weights: its first byte and its first scale.
-struct WRow {
-    const uint8_t* w;
-    const uint8_t* s;
+// Where a chunk lies: US steps from `step` on, of the rows g (+ 8) of R tiles.
+struct WChunk {
+    const uint8_t* w;      // this lane's granule of its first row at step 0
+    const uint8_t* s;      // that row's first scale
+    uint32_t rows;         // bit 2 r + h: row exists (all clear: nothing to fetch)
+    uint32_t step;
 };
 
-template <int F>
-__device__ __forceinline__ void load_gran(AGran<F>& a, int half, const WRow& row, bool valid, uint32_t step,
-                                          int q, uint32_t rb) {
-    const uint32_t off = step * 64u + q * 16u;
-    if (valid && off < rb) {
-        ld_stream(a.w[half], row.w + off);
-        if constexpr (F == kWNvfp4) a.s[half] = __ldg(reinterpret_cast<const uint16_t*>(row.s) + (off >> 4));
-        if constexpr (F == kWMxfp4) a.s[half] = __ldg(row.s + (off >> 4));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a.w[half].w[i] = 0u;
-        if constexpr (WInfo<F>::kFp4) a.s[half] = 0u;
+// Distances in bytes between a lane's rows: from tile to tile, and from row g
+// to row g + 8 of a tile; of the weights and of the scales.
+struct WStride {
+    uint64_t tile_w, half_w, tile_s, half_s;
+};
+
+// A warp's ring of D chunks in shared memory.
+template <int F, int R, int US, int D>
+struct WRing {
+    static constexpr uint32_t kChunk = US * R * 2 * 512;   // bytes
+    static constexpr uint32_t kBytes = kChunk * D;
+    uint32_t base;                                         // this lane's first granule
+    uint32_t slot;                                         // byte offset of the next chunk to read (and refill)
+
+    __device__ __forceinline__ void init(uint8_t* smem) {
+        base = uint32_t(__cvta_generic_to_shared(smem)) + (threadIdx.x % kWarp) * 16u;
+        slot = 0;
     }
-}
+
+    // Start copying a chunk into the slot at byte offset `at`. Granules outside
+    // the matrix are zero-filled and nothing is read for them; chunks that lie
+    // wholly inside (nearly all) skip those tests.
+    __device__ __forceinline__ void fetch(uint32_t at, const WChunk& c, const WStride& st, const uint8_t* any,
+                                          uint32_t rb) {
+        const bool inside = c.rows == (1u << (2 * R)) - 1u && (c.step + US) * 64u <= rb;
+        if (__all_sync(kFull, inside)) {
+            const uint8_t* p = c.w + c.step * 64u;
+#pragma unroll
+            for (int i = 0; i < US; ++i)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + at + ((i * R + r) * 2 + h) * 512u),
+                                     "l"(p + r * st.tile_w + h * st.half_w + i * 64)
+                                     : "memory");
+            return;
+        }
+        const uint32_t q16 = (threadIdx.x % 4) * 16u;
+#pragma unroll 1
+        for (int i = 0; i < US; ++i) {
+            const uint32_t off = (c.step + i) * 64u;
+#pragma unroll 1
+            for (int r = 0; r < R; ++r)
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const bool ok = off + q16 < rb && ((c.rows >> (2 * r + h)) & 1u);
+                    const uint8_t* p = ok ? c.w + r * st.tile_w + h * st.half_w + off : any;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + at + ((i * R + r) * 2 + h) * 512u),
+                                 "l"(p), "r"(ok ? 16 : 0)
+                                 : "memory");
+                }
+        }
+    }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+    // Nothing may be in flight when the block ends.
+    __device__ __forceinline__ static void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+    // Wait for the oldest chunk: all but the D - 1 newest groups are complete.
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); }
+
+    // This lane's granules of tile r at step i of that chunk.
+    __device__ __forceinline__ void read(AGran& a, int i, int r) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(a.w[h].w[0]), "=r"(a.w[h].w[1]), "=r"(a.w[h].w[2]), "=r"(a.w[h].w[3])
+                         : "r"(base + slot + uint32_t((i * R + r) * 2 + h) * 512u)
+                         : "memory");
+    }
+    __device__ __forceinline__ void next() { slot = slot + kChunk == kBytes ? 0u : slot + kChunk; }
+};
+
+// The scales of a chunk's granules (4-bit weights): read ahead by one chunk,
+// 32 bytes of a row's scales serve 4 to 8 steps from L1.
+template <int F, int R, int US>
+struct WScales {
+    uint32_t s[WInfo<F>::kFp4 ? US : 1][R][2];
+
+    __device__ __forceinline__ void load(const WChunk& c, const WStride& st, uint32_t rb) {
+        if constexpr (WInfo<F>::kFp4) {
+            const int q = threadIdx.x % 4;
+            const uint32_t bytes = F == kWNvfp4 ? 2 : 1;   // per granule
+            const bool inside = c.rows == (1u << (2 * R)) - 1u && (c.step + US) * 64u <= rb;
+            const uint8_t* p = c.s + (c.step * 4u + q) * bytes;
+            if (__all_sync(kFull, inside)) {
+#pragma unroll
+                for (int i = 0; i < US; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) s[i][r][h] = one(p + r * st.tile_s + h * st.half_s + i * 4 * bytes);
+            } else {
+#pragma unroll
+                for (int i = 0; i < US; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const bool ok = (c.step + i) * 64u + q * 16u < rb && ((c.rows >> (2 * r + h)) & 1u);
+                            s[i][r][h] = ok ? one(p + r * st.tile_s + h * st.half_s + i * 4 * bytes) : 0u;
+                        }
+            }
+        }
+    }
+
+private:
+    __device__ __forceinline__ static uint32_t one(const uint8_t* p) {
+        if constexpr (F == kWNvfp4) return __ldg(reinterpret_cast<const uint16_t*>(p));
+        else return __ldg(p);
+    }
+};
 
 // One lane's values of its token at one step.
 template <int F>
@@ -112,155 +193,47 @@ __device__ __forceinline__ void load_x(BGran<F>& b, const uint16_t* xrow, bool v
     }
 }
 
-// ---------------------------------------------------------------------------
-// 4-bit weights go through f16 products. E2M1 converts to f16 in hardware (one
-// instruction per two codes; there is none to bfloat16, where placing the bits
-// by shifts and masks costs four), and a weight times its scale is exact in
-// f16. That leaves bfloat16's range to be carried beside the f16 values:
-//  - x: each token's values of one step (128 k) are multiplied by the power of
-//    two that brings their largest into [2^14, 2^15), and the step's float32
-//    sums by its inverse. A value 2^-32 of the step's largest still keeps its 8
-//    bits; what smaller ones lose is under 2^-39 of the largest.
-//  - MXFP4: an E8M0 scale enters as 2^(X - Xmax + 13), Xmax the largest of the
-//    warp's blocks in the step, and 2^(Xmax - 13) multiplies the sums. Blocks
-//    more than 2^27 below the largest take another turn with their own Xmax.
-//  - NVFP4: E4M3 scales and their products with E2M1 are within f16's range.
-// ---------------------------------------------------------------------------
-
-constexpr int kXPairs = 16;   // f16 pairs of one lane's x in a step of 4-bit weights
-
-// One lane's 32 values of its token as f16, times a power of two shared by the
-// token's four lanes; returns the inverse of that power. Infinities and NaN
-// stay what they are.
-__device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXPairs]) {
+// Products of one step, bfloat16 weights: R tiles of 16 rows against the
+// groups of 8 tokens set in `live` (a bit each, the same for the whole warp).
+// tile(a, r) reads a tile's granules, load(n, b) the x of group n.
+template <int R, int NG, typename Tile, typename Load>
+__device__ __forceinline__ void bf16_step(float (&acc)[R][NG][4], uint32_t live, Tile&& tile, Load&& load) {
+    BGran<kWBf16> b[NG];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { h[4 * i] = x[i].x; h[4 * i + 1] = x[i].y; h[4 * i + 2] = x[i].z; h[4 * i + 3] = x[i].w; }
-    uint32_t m = 0;   // |largest| of each half: max of magnitudes, NaN ignored, sign to be dropped
+    for (int n = 0; n < NG; ++n)
+        if (NG == 1 || ((live >> n) & 1u)) load(n, b[n]);
 #pragma unroll
-    for (int i = 0; i < kXPairs; ++i) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(h[i]));
-    m &= 0x7fff7fffu;
-    m = max(m >> 16, m & 0xffffu);
-    m = max(m, __shfl_xor_sync(kFull, m, 1));
-    m = max(m, __shfl_xor_sync(kFull, m, 2));
-    const uint32_t e = min(max(m >> 7, 15u), 254u);                  // biased exponent of the largest
-    const float scale = __uint_as_float((268u - e) << 23);           // 2^(14 - (e - 127))
+    for (int r = 0; r < R; ++r) {
+        AGran a;
+        tile(a, r);
 #pragma unroll
-    for (int i = 0; i < kXPairs; ++i) {
-        float lo, hi;
-        f2_split(mul2(bf16x2_to_f2(h[i]), f2(scale, scale)), lo, hi);
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(hi), "f"(lo));
-    }
-    return __uint_as_float((e - 14u) << 23);                         // 2^(e - 127 - 14)
-}
-
-// Products of one step: R tiles of 16 rows against `groups` groups of 8 tokens
-// (those set in `live`, a bit each, the same for the whole warp). load(n, b)
-// fetches the x of group n; f multiplies the sums of 4-bit weights. With
-// 4-bit weights a further group decodes the weights again: keeping the decoded
-// step (32 registers a tile) or several groups' x (16 each) beside the loads
-// in flight costs more in occupancy than it saves, and an expert seldom has
-// more than 8 of at most 32 tokens.
-template <int F, int R, int NG, typename Load>
-__device__ __forceinline__ void mma_step(float (&acc)[R][NG][4], const AGran<F> (&a)[R], uint32_t live, float f,
-                                         Load&& load) {
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-        if (NG > 1 && !((live >> n) & 1u)) continue;
-        BGran<F> b;
-        load(n, b);
-        if constexpr (F == kWBf16) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                mma_bf16(acc[r][n], a[r].w[0].w[0], a[r].w[1].w[0], a[r].w[0].w[1], a[r].w[1].w[1], b.x[0].x, b.x[0].y);
-                mma_bf16(acc[r][n], a[r].w[0].w[2], a[r].w[1].w[2], a[r].w[0].w[3], a[r].w[1].w[3], b.x[0].z, b.x[0].w);
-            }
-        } else {
-            const int q = threadIdx.x % 4;
-            uint32_t h[kXPairs];
-            const float inv = x_to_f16(b.x, h) * f;
-            // of this lane's two tokens in C, 2 q and 2 q + 1
-            const float f0 = __shfl_sync(kFull, inv, 8 * q), f1 = __shfl_sync(kFull, inv, 8 * q + 4);
-            uint32_t todo = ~0u;    // MXFP4: the blocks (bit 2 r + half) still to be added
-            while (true) {
-                float g0 = f0, g1 = f1;
-                uint32_t top = 0;
-                if constexpr (F == kWMxfp4) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (((todo >> (2 * r + k)) & 1u) && a[r].s[k] != 255u) top = max(top, a[r].s[k]);
-                    top = __reduce_max_sync(kFull, top);
-                    // 2^(top - 127 - 13), a subnormal float for top < 14
-                    const float fx = top >= 14u ? __uint_as_float((top - 13u) << 23) : __uint_as_float(1u << (top + 9u));
-                    g0 *= fx;
-                    g1 *= fx;
-                }
-                uint32_t far = 0;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    uint32_t s[2][2];   // the scales of k 0..15 and 16..31 of the granule, in both halves
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if constexpr (F == kWNvfp4) {
-                            uint32_t v;
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"(uint16_t(a[r].s[k])));
-                            s[k][0] = __byte_perm(v, v, 0x1010);
-                            s[k][1] = __byte_perm(v, v, 0x3232);
-                        } else {
-                            const uint32_t x = a[r].s[k];
-                            const int d = int(x) - int(top) + 28;      // biased f16 exponent
-                            const bool mine = (todo >> (2 * r + k)) & 1u;
-                            uint32_t v = d >= 1 ? uint32_t(d) * 0x04000400u : 0u;
-                            if (x == 255u) v = 0x7e007e00u;            // NaN
-                            s[k][0] = s[k][1] = mine ? v : 0u;
-                            far |= uint32_t(mine && d < 1) << (2 * r + k);
-                        }
-                    }
-                    float c[4] = {};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t p0[4], p1[4];
-                        e2m1_to_f16(a[r].w[0].w[j], s[0][j / 2], p0);
-                        e2m1_to_f16(a[r].w[1].w[j], s[1][j / 2], p1);
-                        mma_f16(c, p0[0], p1[0], p0[1], p1[1], h[4 * j], h[4 * j + 1]);
-                        mma_f16(c, p0[2], p1[2], p0[3], p1[3], h[4 * j + 2], h[4 * j + 3]);
-                    }
-                    acc[r][n][0] = fmaf(c[0], g0, acc[r][n][0]);
-                    acc[r][n][1] = fmaf(c[1], g1, acc[r][n][1]);
-                    acc[r][n][2] = fmaf(c[2], g0, acc[r][n][2]);
-                    acc[r][n][3] = fmaf(c[3], g1, acc[r][n][3]);
-                }
-                if constexpr (F == kWNvfp4) break;
-                if (!__any_sync(kFull, far != 0u)) break;
-                // blocks far below the largest: another turn, unless all their codes are zero
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const Bits<16>& w = a[r].w[k];
-                        if (((w.w[0] | w.w[1] | w.w[2] | w.w[3]) & 0x77777777u) == 0u) far &= ~(1u << (2 * r + k));
-                    }
-                todo = far;
-                if (!__any_sync(kFull, todo != 0u)) break;
-            }
+        for (int n = 0; n < NG; ++n) {
+            if (NG > 1 && !((live >> n) & 1u)) continue;
+            mma_bf16(acc[r][n], a.w[0].w[0], a.w[1].w[0], a.w[0].w[1], a.w[1].w[1], b[n].x[0].x, b[n].x[0].y);
+            mma_bf16(acc[r][n], a.w[0].w[2], a.w[1].w[2], a.w[0].w[3], a.w[1].w[3], b[n].x[0].z, b[n].x[0].w);
         }
     }
 }
 
 // A warp's accumulators -> its part of the block's partial sums
-// s_red[warp][token][row], rows 0..16 R - 1 (C fragment: lane (g, q) holds
-// rows g, g + 8 of tokens 2 q, 2 q + 1).
+// s_red[warp][token][row], rows 0..16 R - 1 of the first `cols` tokens (C
+// fragment: lane (g, q) holds rows g, g + 8 of tokens 2 q, 2 q + 1).
 template <int R, int NG>
-__device__ __forceinline__ void store_partial(float* s_warp, const float (&acc)[R][NG][4]) {
+__device__ __forceinline__ void store_partial(float* s_warp, const float (&acc)[R][NG][4], int cols) {
     const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int z = 0; z < 2; ++z) {
+            const int c = n * 8 + 2 * q + z;
+            if (c < cols) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s_warp[(n * 8 + 2 * q + (i & 1)) * (16 * R) + r * 16 + g + (i >> 1) * 8] = acc[r][n][i];
+                for (int r = 0; r < R; ++r) {
+                    s_warp[c * (16 * R) + r * 16 + g] = acc[r][n][z];
+                    s_warp[c * (16 * R) + r * 16 + g + 8] = acc[r][n][z + 2];
+                }
+            }
+        }
 }
 
 // ---------------------------------------------------------------------------

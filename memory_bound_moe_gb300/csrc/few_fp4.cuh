@@ -1,0 +1,553 @@
+// Products of a few tokens with 4-bit weights: the streaming core of
+// moe_gemv_fp4 and of both kernels of moe_layer_fp4.
+//
+// Numbers. E2M1 converts to f16 in hardware (one instruction per two codes;
+// there is none to bfloat16, where placing the bits by shifts and masks costs
+// four), and a weight times its scale is exact in f16, so the products are
+// m16n8k16 f16 with float32 sums. bfloat16's range is carried beside the f16
+// values:
+//  - x: each token's values of one step (128 k) are multiplied by the power of
+//    two that brings their largest into [2^14, 2^15), and the step's sums by
+//    its inverse. A value 2^-32 of the step's largest still keeps its 8 bits;
+//    what smaller ones lose is under 2^-39 of the largest.
+//  - MXFP4: an E8M0 scale enters as 2^(X - Xmax + 13), Xmax the largest of the
+//    warp's blocks in the step, and 2^(Xmax - 13) multiplies the sums. Where
+//    blocks lie more than 2^27 apart they take turns, each with its own Xmax.
+//  - NVFP4: E4M3 scales and their products with E2M1 are within f16's range.
+//
+// Work. Next to the loads what bounds it is the arithmetic logic pipe: 16 lanes
+// a clock, 4 conversions per 8 weights and lane, and every further integer
+// operation at the same price (the matrix instructions and the scale products
+// have pipes of their own). So the loop over k holds little else:
+//  - a warp takes a tile of 16 rows; a lane takes 64 contiguous bytes (128 k) of
+//    each of its two rows, a "chunk" of 512 k per warp, in two 256-bit loads,
+//    their scales in one. A chunk is four steps of 128 k, granule i of every
+//    lane making step i. The next chunk's loads go out as soon as half of the
+//    registers is used up; 24 warps of 80 registers on an SM hide the rest.
+//  - x is converted once per block, into shared memory, in the order the B
+//    fragments are read: all distances in the loop are constants. (With the
+//    same data in global memory behind run-time strides the loop took 24
+//    instructions per matrix instruction instead of 13.)
+// Measured on GB300 with the inner loop alone (57344 x 4096 weights, 132 MB,
+// one wave): loads without products 24.6 us, products without loads 22.9 us;
+// together 26.9 us with 24 warps of 80 registers, 30.9 us with 16 of 128, and
+// 34.1 us with two tiles per warp and 16 warps.
+#pragma once
+
+#include "few_device.cuh"
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+namespace moe {
+
+constexpr int kXPairs = 16;         // f16 pairs of one lane's x in a step
+constexpr uint32_t kChunkK = 512;   // k per chunk
+
+#ifndef MOE_FP4_WNV
+#define MOE_FP4_WNV 20
+#endif
+#ifndef MOE_FP4_WMX
+#define MOE_FP4_WMX 16
+#endif
+// Blocks are one per SM, of up to kMaxWarps warps (what the registers allow),
+// in RG row groups x KS splits of k.
+constexpr uint32_t kUnits = 88;                       // (group, step) units of x that shared memory holds
+constexpr uint32_t kUnit = 2048;                      // one unit: 8 tokens x 128 k, f16
+constexpr uint32_t kInvAt = kUnits * kUnit;           // the units' inverse powers of two, 8 each
+constexpr uint32_t kPartAt = kInvAt + kUnits * 32u;   // partial sums: [warp][8 NG tokens][16 rows]
+
+template <int F, int NG>
+struct Fp4Block {
+    static constexpr int kMaxWarps = NG == 1 ? (F == kWNvfp4 ? MOE_FP4_WNV : MOE_FP4_WMX) : 16;
+    static constexpr int kMaxThreads = kMaxWarps * kWarp;
+    static constexpr uint32_t kSmem = kPartAt + kMaxWarps * NG * 512u;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The 8 E2M1 codes of w times scale (an f16 in both halves) as f16 pairs
+// (codes 2 i, 2 i + 1). Exact: 2 significant bits times at most 4.
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t scale, uint32_t (&p)[4]) {
+    asm("{.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(p[i]) : "r"(scale));
+}
+
+// One lane's 32 values of its token as f16, times a power of two shared by the
+// token's four lanes; returns the inverse of that power. Infinities and NaN
+// stay what they are.
+__device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXPairs]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { h[4 * i] = x[i].x; h[4 * i + 1] = x[i].y; h[4 * i + 2] = x[i].z; h[4 * i + 3] = x[i].w; }
+    uint32_t m = 0;   // |largest| of each half: max of magnitudes, NaN ignored, sign to be dropped
+#pragma unroll
+    for (int i = 0; i < kXPairs; ++i) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(h[i]));
+    m &= 0x7fff7fffu;
+    m = max(m >> 16, m & 0xffffu);
+    m = max(m, __shfl_xor_sync(kFull, m, 1));
+    m = max(m, __shfl_xor_sync(kFull, m, 2));
+    const uint32_t e = min(max(m >> 7, 15u), 254u);                  // biased exponent of the largest
+    const float scale = __uint_as_float((268u - e) << 23);           // 2^(14 - (e - 127))
+#pragma unroll
+    for (int i = 0; i < kXPairs; ++i) {
+        float lo, hi;
+        f2_split(mul2(bf16x2_to_f2(h[i]), f2(scale, scale)), lo, hi);
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(hi), "f"(lo));
+    }
+    return __uint_as_float((e - 14u) << 23);                         // 2^(e - 127 - 14)
+}
+
+// 2^(x - 127 - 13), a subnormal float for x < 14.
+__device__ __forceinline__ float mxfp4_unit(uint32_t x) {
+    return x >= 14u ? __uint_as_float((x - 13u) << 23) : __uint_as_float(1u << (x + 9u));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// One unit of x: step i of chunk `chunk` of 8 rows (row: the lane group's, NULL
+// gives zeros), by one warp, to unit `to` of shared memory: for j = 0..3 the 16
+// bytes that every lane reads for word j of its granule.
+__device__ __forceinline__ void stage_unit(uint8_t* smem, uint32_t to, const uint16_t* row, uint32_t K, uint32_t chunk, uint32_t i) {
+    const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
+    const uint32_t k0 = chunk * kChunkK + q * 128u + i * 32u;
+    uint4 x[4] = {};
+    if (row != nullptr && k0 < K) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z) x[z] = __ldg(reinterpret_cast<const uint4*>(row + k0) + z);
+    }
+    uint32_t h[kXPairs];
+    const float inv = x_to_f16(x, h);
+    uint4* p = reinterpret_cast<uint4*>(smem + to * kUnit) + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j * 32] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+    if (q == 0) reinterpret_cast<float*>(smem + kInvAt)[to * 8 + g] = inv;
+}
+
+// One lane's weights of a chunk: 64 bytes of its rows g and g + 8 of a tile,
+// and their scales as stored (4 E8M0 or 8 E4M3 bytes).
+template <int F>
+struct WChunk4 {
+    Bits<32> w[2][2];                        // [row half][half of the 64 bytes]
+    uint32_t s[2][F == kWNvfp4 ? 2 : 1];
+};
+
+// Where a lane's rows lie: its 64 bytes of row g in chunk 0, their scales, and
+// the distances to row g + 8.
+struct Place4 {
+    const uint8_t* w;
+    const uint8_t* s;
+    uint32_t rows;       // bit h: row g + 8 h exists
+};
+struct Shape4 {
+    uint64_t half_w, half_s;
+    uint32_t rb;         // bytes of a row
+    uint32_t whole;      // chunks that lie wholly in a row, if rows may be read in 32-byte pieces (else 0)
+    int scale_align;     // bytes: at most those of a lane's scales (4 or 8)
+};
+
+template <int F>
+__device__ __forceinline__ Shape4 fp4_shape(uint64_t half_rows, uint32_t K, const void* w) {
+    const uint32_t rb = row_bytes<F>(K), rs = row_scales<F>(K);
+    const uint32_t al = rs & (0u - rs);   // largest power of two that divides a row's scales
+    const bool wide = rb % 32u == 0u && reinterpret_cast<uintptr_t>(w) % 32u == 0u;
+    return {half_rows * rb, half_rows * rs, rb, wide ? rb / 256u : 0u, int(min(al, F == kWNvfp4 ? 8u : 4u))};
+}
+
+// This lane's granules of chunk c that lie in the row.
+__device__ __forceinline__ uint32_t granules4(const Shape4& sh, uint32_t c) {
+    const uint32_t at = c * 256u + (threadIdx.x % 4) * 64u;
+    return at < sh.rb ? min((sh.rb - at) / 16u, 4u) : 0u;
+}
+
+// Half `half` (32 bytes per row) of chunk c, at p.w. `whole`: nothing of it is
+// cut off by the end of the row or of the matrix (nearly always), and rows may
+// be read in 32-byte pieces.
+template <int F>
+__device__ __forceinline__ void load_half(WChunk4<F>& a, int half, const Place4& p, const Shape4& sh, uint32_t c, bool whole) {
+    if (whole) {
+        ld_stream(a.w[0][half], p.w + half * 32);
+        ld_stream(a.w[1][half], p.w + sh.half_w + half * 32);
+        return;
+    }
+    const uint32_t n = granules4(sh, c);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            Bits<16> v;
+            if (((p.rows >> h) & 1u) && uint32_t(2 * half + i) < n) ld_stream(v, p.w + h * sh.half_w + half * 32 + i * 16);
+            else v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0u;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) a.w[h][half].w[4 * i + z] = v.w[z];
+        }
+}
+
+template <int F>
+__device__ __forceinline__ void load_scales(WChunk4<F>& a, const Place4& at, const Shape4& sh, uint32_t c, bool whole) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t* p = at.s + h * sh.half_s;
+        if (!whole) {
+            const uint32_t n = (at.rows >> h) & 1u ? granules4(sh, c) : 0u;
+            a.s[h][0] = 0u;
+            if constexpr (F == kWNvfp4) a.s[h][1] = 0u;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                if (i < n) {
+                    if constexpr (F == kWNvfp4) a.s[h][i / 2] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
+                    else a.s[h][0] |= uint32_t(__ldg(p + i)) << (8 * i);
+                }
+            continue;
+        }
+        if constexpr (F == kWNvfp4) {
+            if (sh.scale_align == 8) {
+                const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
+                a.s[h][0] = t.x;
+                a.s[h][1] = t.y;
+            } else if (sh.scale_align == 4) {
+                a.s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+                a.s[h][1] = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
+            } else {
+                const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
+                a.s[h][0] = __ldg(v) | uint32_t(__ldg(v + 1)) << 16;
+                a.s[h][1] = __ldg(v + 2) | uint32_t(__ldg(v + 3)) << 16;
+            }
+        } else {
+            if (sh.scale_align == 4) {
+                a.s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            } else if (sh.scale_align == 2) {
+                const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
+                a.s[h][0] = __ldg(v) | uint32_t(__ldg(v + 1)) << 16;
+            } else {
+                a.s[h][0] = __ldg(p) | uint32_t(__ldg(p + 1)) << 8 | uint32_t(__ldg(p + 2)) << 16 | uint32_t(__ldg(p + 3)) << 24;
+            }
+        }
+    }
+}
+
+// MXFP4 blocks further apart than one window, with a NaN scale, or so small
+// that the factors' product could leave float32: turn by turn, each with the
+// largest scale among the blocks not yet added. Adds one group's products of a
+// step (its B fragments at xb) to acc; w [2][4] codes, sc [2] scales.
+static __device__ __noinline__ void mxfp4_apart(float* acc, const uint32_t* w, const uint32_t* sc, uint32_t xb, float f0, float f1) {
+    uint32_t todo = 3u;
+    while (__any_sync(kFull, todo != 0u)) {
+        uint32_t top = 0;
+        for (int k = 0; k < 2; ++k)
+            if (((todo >> k) & 1u) && sc[k] != 255u) top = max(top, sc[k]);
+        top = __reduce_max_sync(kFull, top);
+        const float fx = mxfp4_unit(top);
+        uint32_t s[2], left = 0;
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t* v = w + k * 4;
+            const int d = int(sc[k]) - int(top) + 28;   // biased f16 exponent
+            s[k] = 0;
+            if ((todo >> k) & 1u) {
+                if (sc[k] == 255u) s[k] = 0x7e007e00u;     // NaN
+                else if (d >= 1) s[k] = uint32_t(d) * 0x04000400u;
+                else if (((v[0] | v[1] | v[2] | v[3]) & 0x77777777u) != 0u) left |= 1u << k;
+            }
+        }
+        float c[4] = {};
+        for (int j = 0; j < 4; ++j) {
+            uint32_t p0[4], p1[4];
+            e2m1_to_f16(w[j], s[0], p0);
+            e2m1_to_f16(w[4 + j], s[1], p1);
+            const uint4 b = lds128(xb + j * 512u);
+            mma_f16(c, p0[0], p1[0], p0[1], p1[1], b.x, b.y);
+            mma_f16(c, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
+        }
+        for (int z = 0; z < 4; ++z) {
+            const float f = z & 1 ? f1 : f0;   // the smaller of the factors last: neither product leaves the range
+            acc[z] += f <= 1.0f ? (c[z] * f) * fx : (c[z] * fx) * f;
+        }
+        todo = left;
+    }
+}
+
+// MXFP4: the largest scale of chunk c's blocks over the warp, and whether they
+// need turns. Granules that are cut off (their codes are zero) take the largest
+// scale for theirs.
+__device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole) {
+    uint32_t top = 0, low = 255u;
+    if (!whole) {
+        const uint32_t n = granules4(sh, c);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, (a.s[h][0] >> (8 * i)) & 255u);
+        top = __reduce_max_sync(kFull, top);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t m = (p.rows >> h) & 1u ? n : 0u, in = m == 4u ? ~0u : (1u << (8u * m)) - 1u;
+            a.s[h][0] |= top * 0x01010101u & ~in;
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = __byte_perm(a.s[h][0], 0, 0x4440 + i);
+            top = max(top, x);
+            low = min(low, x);
+        }
+    top = __reduce_max_sync(kFull, top);
+    apart = __any_sync(kFull, low + 28u <= top) || top == 255u || top < 32u;
+    return top;
+}
+
+// The products of step i of a chunk with the first `groups` groups of 8 tokens.
+// xb[n]: this lane's B fragments of group n in the chunk's first unit, inv[n]:
+// that unit's inverse powers of two of the lane's two tokens in C, 2 q and 2 q
+// + 1; f multiplies the sums, top and apart as of mxfp4_top.
+template <int F, int NG>
+__device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& a, const uint32_t (&sc)[2][F == kWNvfp4 ? 2 : 1],
+                                         int i, const uint32_t (&xb)[NG], const float* (&inv)[NG], int groups, float f,
+                                         uint32_t top, bool apart) {
+    uint32_t s[2][2];   // f16 scale in both halves: [row g or g + 8][k 0..15 or 16..31 of the granule]
+    if constexpr (F == kWNvfp4) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t v;
+            asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}"
+                : "=r"(v) : "r"(i % 2 ? sc[k][i / 2] >> 16 : sc[k][i / 2]));
+            s[k][0] = __byte_perm(v, v, 0x1010);
+            s[k][1] = __byte_perm(v, v, 0x3232);
+        }
+    } else {
+        if (apart) {
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                if (NG > 1 && n >= groups) break;
+                const float2 v = *reinterpret_cast<const float2*>(inv[n] + i * 8);
+                float t[4];
+                uint32_t w[2][4], x[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    x[h] = (sc[h][0] >> (8 * i)) & 255u;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) w[h][z] = a.w[h][i / 2].w[(i % 2) * 4 + z];
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) t[z] = acc[n][z];
+                mxfp4_apart(t, &w[0][0], x, xb[n] + i * kUnit, v.x * f, v.y * f);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) acc[n][z] = t[z];
+            }
+            return;
+        }
+        f *= mxfp4_unit(top);
+        const uint32_t shift = (28u - top) * 0x04000400u;   // biased f16 exponent X - top + 28, in both halves
+#pragma unroll
+        for (int k = 0; k < 2; ++k) s[k][0] = s[k][1] = __byte_perm(sc[k][0], 0, 0x4440 + i) * 0x04000400u + shift;
+    }
+    float c[NG][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t p[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) e2m1_to_f16(a.w[k][i / 2].w[(i % 2) * 4 + j], s[k][j / 2], p[k]);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            if (NG > 1 && n >= groups) break;
+            const uint4 b = lds128(xb[n] + i * kUnit + j * 512u);
+            mma_f16(c[n], p[0][0], p[1][0], p[0][1], p[1][1], b.x, b.y);
+            mma_f16(c[n], p[0][2], p[1][2], p[0][3], p[1][3], b.z, b.w);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+        if (NG > 1 && n >= groups) break;
+        const float2 v = *reinterpret_cast<const float2*>(inv[n] + i * 8);
+        const float f0 = v.x * f, f1 = v.y * f;
+        acc[n][0] = fmaf(c[n][0], f0, acc[n][0]);
+        acc[n][1] = fmaf(c[n][1], f1, acc[n][1]);
+        acc[n][2] = fmaf(c[n][2], f0, acc[n][2]);
+        acc[n][3] = fmaf(c[n][3], f1, acc[n][3]);
+    }
+}
+
+// The chunks c0 .. c1 - 1 of one tile; x of chunk c0 begins at unit u0 of
+// shared memory, each group's `group_units` behind the one before.
+template <int F, int NG>
+__device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Shape4& sh, uint32_t c0, uint32_t c1,
+                                         uint8_t* smem, uint32_t u0, uint32_t group_units, int groups, float f) {
+    if (c0 >= c1) return;
+    const int lane = threadIdx.x % kWarp, q = lane % 4;
+    uint32_t xb[NG];
+    const float* inv[NG];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+        const uint32_t u = u0 + n * group_units;
+        xb[n] = uint32_t(__cvta_generic_to_shared(smem)) + u * kUnit + lane * 16u;
+        inv[n] = reinterpret_cast<const float*>(smem + kInvAt) + u * 8 + 2 * q;
+    }
+    const uint32_t whole = __all_sync(kFull, p.rows == 3u) ? sh.whole : 0u;   // chunks below it are whole
+    p.w += c0 * 256u;
+    p.s += c0 * (kChunkK / WInfo<F>::kBlock);
+    WChunk4<F> a;
+    load_half(a, 0, p, sh, c0, c0 < whole);
+    load_half(a, 1, p, sh, c0, c0 < whole);
+    load_scales(a, p, sh, c0, c0 < whole);
+#pragma unroll 1
+    for (uint32_t c = c0; c < c1; ++c) {
+        uint32_t top = 0;
+        bool apart = false;
+        if constexpr (F == kWMxfp4) top = mxfp4_top(a, apart, p, sh, c, c < whole);
+        uint32_t sc[2][F == kWNvfp4 ? 2 : 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int z = 0; z < (F == kWNvfp4 ? 2 : 1); ++z) sc[h][z] = a.s[h][z];
+        const bool more = c + 1 < c1;
+        p.w += 256;
+        p.s += kChunkK / WInfo<F>::kBlock;
+        if (more) load_scales(a, p, sh, c + 1, c + 1 < whole);
+        fp4_step<F, NG>(acc, a, sc, 0, xb, inv, groups, f, top, apart);
+        fp4_step<F, NG>(acc, a, sc, 1, xb, inv, groups, f, top, apart);
+        if (more) load_half(a, 0, p, sh, c + 1, c + 1 < whole);
+        fp4_step<F, NG>(acc, a, sc, 2, xb, inv, groups, f, top, apart);
+        fp4_step<F, NG>(acc, a, sc, 3, xb, inv, groups, f, top, apart);
+        if (more) load_half(a, 1, p, sh, c + 1, c + 1 < whole);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            xb[n] += 4 * kUnit;
+            inv[n] += 32;
+        }
+    }
+}
+
+// Barrier of the KS warps of row group rg.
+__device__ __forceinline__ void group_sync(int rg, int KS) {
+    if (KS == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(rg + 1), "r"(KS * kWarp) : "memory");
+}
+
+// One group's accumulators -> [token][row], 16 rows.
+template <int NG>
+__device__ __forceinline__ void store_group(float* p, const float (&acc)[NG][4], int n) {
+    const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+        if (k == n) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) p[(2 * q + (z & 1)) * 16 + g + (z >> 1) * 8] = acc[k][z];
+        }
+}
+
+// Sum over the KS splits of k (warps rg KS ..) of element i of their `stride`
+// floats.
+__device__ __forceinline__ float sum_splits(const float* s_part, int rg, int KS, int stride, int i) {
+    const float* p = s_part + rg * KS * stride + i;
+    float v = p[0];
+    for (int k = 1; k < KS; ++k) v += p[k * stride];
+    return v;
+}
+
+// Clusters of C blocks (C = 1 .. 8) of a kernel that one device holds at once,
+// asked once per device: with one block per SM and the SMs of a graphics
+// cluster in odd numbers, far fewer than SMs / C (a GEMV in clusters of 7 ran
+// in three waves).
+struct ClusterSlots {
+    std::atomic<uint64_t> known[64] = {};   // per device: 8 bytes, min(slots, 255)
+
+    template <typename Kernel>
+    cudaError_t get(Kernel kernel, uint32_t threads, size_t smem, int num_sms, uint32_t (&slots)[9]) {
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        uint64_t v = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+        if (v == 0) {
+            for (uint32_t c = 1; c <= 8; ++c) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(c * 8);
+                cfg.blockDim = dim3(threads);
+                cfg.dynamicSmemBytes = smem;
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = c;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int n = num_sms;
+                if (c > 1) {
+                    err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+                    if (err != cudaSuccess) return err;
+                }
+                v |= uint64_t(std::max(1, std::min(n, 255))) << (8 * (c - 1));
+            }
+            if (dev < 64) known[dev].store(v, std::memory_order_relaxed);
+        }
+        for (uint32_t c = 1; c <= 8; ++c) slots[c] = uint32_t(v >> (8 * (c - 1))) & 255u;
+        return cudaSuccess;
+    }
+};
+
+// How a kernel of one block per SM over `tiles` row tiles divides its work: W
+// warps per block, KS splits of k in a block, C blocks of a cluster, that share
+// the `chunks` of a tile. The least of a simple estimate in microseconds: a
+// wave of blocks pays about 2.5 for launch and sums (1 more for a cluster),
+// 0.4 per unit of x a warp converts, and per chunk 0.25 for every warp of a
+// scheduler, but no less than a load's latency, 1.0.
+struct Fp4Split {
+    uint32_t w, ks, c;
+};
+inline Fp4Split fp4_split(uint64_t tiles, uint32_t chunks, uint32_t groups, uint32_t max_warps, const uint32_t (&slots)[9]) {
+    Fp4Split best = {max_warps, 1, 1};
+    double least = 1e30;
+    for (uint32_t w = 4; w <= max_warps; w += 4)
+        for (uint32_t ks = 1; ks <= w && ks <= chunks; ++ks) {
+            if (w % ks != 0) continue;
+            for (uint32_t c = 1; c <= 8 && (c == 1 || c * ks <= chunks); ++c) {
+                const uint32_t rg = w / ks, share = (chunks + c - 1) / c;
+                const uint64_t waves = ((tiles + rg - 1) / rg + slots[c] - 1) / slots[c];
+                const double chunk = std::max(1.0, 0.25 * (w / 4.0) * (0.6 + 0.4 * groups));
+                const double convert = 0.4 * ((share * 4 * groups + w - 1) / w);
+                const double t = double(waves) * (2.5 + (c > 1 ? 1.0 : 0.0) + convert + chunk * ((share + ks - 1) / ks));
+                if (t < least * 0.98) {
+                    least = t;
+                    best = {w, ks, c};
+                }
+            }
+        }
+    return best;
+}
+
+// s_sum[T][rows] summed over the C blocks of the cluster, in rank order, to
+// store(t, row, value).
+template <typename Store>
+__device__ __forceinline__ void cluster_store(const float* s_sum, int total, int rows, uint32_t rank, uint32_t C, Store&& store) {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    for (int o = int(threadIdx.x + rank * blockDim.x); o < total; o += int(blockDim.x * C)) {
+        float v;
+        if (C > 1) {
+            v = ld_cluster(s_sum + o, 0);
+            for (uint32_t c = 1; c < C; ++c) v += ld_cluster(s_sum + o, c);
+        } else {
+            v = s_sum[o];
+        }
+        store(o / rows, o % rows, v);
+    }
+    if (C > 1) cluster_sync();   // the others may still read this block's sums
+}
+
+}  // namespace moe

@@ -3,19 +3,16 @@
 // W in the library's MXFP4 or NVFP4 layout (codes [N, K/2], scales
 // [N, K/block]). Bound by the weights' bytes (0.53 or 0.56 per value).
 //
-// A block takes 16 R rows; its 8 warps, and the C blocks of its cluster, split
-// k in units of U steps (few_device.cuh). The partial sums meet in shared
-// memory, then through distributed shared memory, always in the same order:
-// results do not depend on timing.
-#include "few_device.cuh"
+// A block takes 16 rows per row group; its row groups share x, its
+// KS splits and the C blocks of its cluster share k (few_fp4.cuh). The partial sums meet
+// in shared memory, then through distributed shared memory, always in the same
+// order: results do not depend on timing.
+#include "few_fp4.cuh"
 #include "moe_launch.h"
 #include "rows_common.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kNw = 8;             // warps per block
-constexpr int kNt = kNw * kWarp;
 
 struct GemvArgs {
     const uint16_t* x;
@@ -23,90 +20,82 @@ struct GemvArgs {
     const uint8_t* scales;
     void* y;
     uint32_t T, N, K;
-    uint32_t units;    // units of U steps along k
+    uint32_t chunks;   // of k in all
     float inv_g;       // 1 / tensor scale (1 for MXFP4)
     int y_f32;
 };
 
-template <int F, int R, int NG, int U>
-__global__ void __launch_bounds__(kNt, 2) gemv_kernel(GemvArgs a, uint32_t C) {
-    extern __shared__ float s_red[];             // [kNw][8 NG][16 R]
-    constexpr int kOut = 8 * NG * 16 * R;
-    pdl_wait_and_release();
+// k is taken slice by slice (what shared memory holds of x; usually all of the
+// block's share), each converted by the whole block first.
+template <int F, int NG>
+__global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) gemv_kernel(GemvArgs a, int KS, uint32_t C) {
+    extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, q = lane % 4;
-    const uint32_t rank = blockIdx.x % C, row0 = blockIdx.x / C * (16 * R);
-    const uint32_t rb = row_bytes<F>(a.K), rs = row_scales<F>(a.K);
-    float acc[R][NG][4] = {};
-    for (uint32_t u = rank * kNw + warp; u < a.units; u += C * kNw) {
-        AGran<F> w[U][R];
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t row = row0 + r * 16 + h * 8 + g;
-                    const WRow p = {a.codes + uint64_t(row) * rb, a.scales + uint64_t(row) * rs};
-                    load_gran<F>(w[i][r], h, p, row < a.N, u * U + i, q, rb);
-                }
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            mma_step<F, R, NG>(acc, w[i], ~0u, 1.0f, [&](int n, BGran<F>& b) {
-                load_x<F>(b, a.x + uint64_t(n * 8 + g) * a.K, n * 8 + g < a.T, u * U + i, q, a.K);
-            });
-    }
-    store_partial<R, NG>(s_red + warp * kOut, acc);
-    __syncthreads();
-    if (C > 1) {
-        for (int o = threadIdx.x; o < kOut; o += kNt) {
-            float s = s_red[o];
-#pragma unroll
-            for (int w = 1; w < kNw; ++w) s += s_red[w * kOut + o];
-            s_red[o] = s;   // this thread alone reads and writes column o
+    const int W = blockDim.x / kWarp, rg = warp / KS, ks = warp % KS, rows = W / KS * 16, T = int(a.T), groups = (T + 7) / 8;
+    const uint32_t rank = blockIdx.x % C, row0 = blockIdx.x / C * rows, mine = row0 + rg * 16 + g;
+    const uint32_t c0 = a.chunks * rank / C, c1 = a.chunks * (rank + 1) / C;
+    float* s_part = reinterpret_cast<float*>(smem + kPartAt);
+    float* s_sum = reinterpret_cast<float*>(smem);   // [T][rows], in the place of x at the end
+    const Shape4 sh = fp4_shape<F>(8, a.K, a.codes);
+    const Place4 p = {a.codes + uint64_t(mine) * sh.rb + q * 64,
+                      a.scales + uint64_t(mine) * row_scales<F>(a.K) + q * (128 / WInfo<F>::kBlock),
+                      uint32_t(mine < a.N) | uint32_t(mine + 8 < a.N) << 1};
+    pdl_wait_and_release();
+    float acc[NG][4] = {};
+    const uint32_t slice = kUnits / 4 / groups;
+    for (uint32_t s0 = c0; s0 < c1; s0 += slice) {
+        const uint32_t n = min(slice, c1 - s0), per = n * 4;
+        if (s0 > c0) __syncthreads();
+        for (uint32_t u = warp; u < per * groups; u += W) {
+            const uint32_t gr = u / per, r = gr * 8 + g;
+            stage_unit(smem, u, r < a.T ? a.x + uint64_t(r) * a.K : nullptr, a.K, s0 + (u - gr * per) / 4, u % 4);
         }
-        cluster_sync();
+        __syncthreads();
+        const uint32_t k0 = n * ks / KS, k1 = n * (ks + 1) / KS;
+        fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups, 1.0f);
     }
-    for (int o = threadIdx.x + (C > 1 ? int(rank) * kNt : 0); o < kOut; o += kNt * int(C)) {
-        float s;
-        if (C > 1) {
-            s = ld_cluster(s_red + o, 0);
-            for (uint32_t c = 1; c < C; ++c) s += ld_cluster(s_red + o, c);
-        } else {
-            s = s_red[o];
-#pragma unroll
-            for (int w = 1; w < kNw; ++w) s += s_red[w * kOut + o];
-        }
-        const uint32_t t = uint32_t(o) / (16 * R), row = row0 + uint32_t(o) % (16 * R);
-        if (t < a.T && row < a.N) {
-            s *= a.inv_g;
-            const uint64_t at = uint64_t(t) * a.N + row;
-            if (a.y_f32) static_cast<float*>(a.y)[at] = s;
-            else static_cast<uint16_t*>(a.y)[at] = uint16_t(pack_bf16x2(s, 0.0f));
+    for (int n = 0; n < groups; ++n) {
+        __syncthreads();
+        store_group<NG>(s_part + warp * 128, acc, n);
+        __syncthreads();
+        for (int o = threadIdx.x; o < 8 * rows; o += blockDim.x) {
+            const int c = o / rows, i = o % rows;
+            if (n * 8 + c < T) s_sum[(n * 8 + c) * rows + i] = sum_splits(s_part, i / 16, KS, 128, c * 16 + i % 16);
         }
     }
-    if (C > 1) cluster_sync();   // the others may still read this block's sums
+    cluster_store(s_sum, T * rows, rows, rank, C, [&](int t, int i, float v) {
+        const uint32_t row = row0 + i;
+        if (row < a.N) {
+            v *= a.inv_g;
+            const uint64_t to = uint64_t(t) * a.N + row;
+            if (a.y_f32) static_cast<float*>(a.y)[to] = v;
+            else static_cast<uint16_t*>(a.y)[to] = uint16_t(pack_bf16x2(v, 0.0f));
+        }
+    });
 }
 
-template <int F, int R, int NG>
-cudaError_t launch_r(GemvArgs a, int num_sms, cudaStream_t stream) {
-    constexpr int U = 2;
-    auto kernel = gemv_kernel<F, R, NG, U>;
-    constexpr size_t smem = sizeof(float) * kNw * 8 * NG * 16 * R;
-    const uint32_t steps = (row_bytes<F>(a.K) + 63) / 64;
-    a.units = (steps + U - 1) / U;
-    const uint32_t tiles = (a.N + 16 * R - 1) / (16 * R);
-    // split k over a cluster until two blocks per SM are busy and while every warp still has a unit
-    uint32_t C = 1;
-    while (C < 8 && tiles * C < 2u * uint32_t(num_sms) && a.units >= 2 * C * kNw) C *= 2;
-    return launch_cluster(kernel, dim3(tiles * C), dim3(kNt), C, smem, stream, a, C);
+template <int F, int NG>
+cudaError_t launch_ng(GemvArgs a, int num_sms, cudaStream_t stream) {
+    auto kernel = gemv_kernel<F, NG>;
+    using B = Fp4Block<F, NG>;
+    static SmemGrant grant;
+    static ClusterSlots clusters;
+    uint32_t slots[9];
+    cudaError_t err = grant.ensure(kernel);
+    if (err == cudaSuccess) err = clusters.get(kernel, B::kMaxThreads, B::kSmem, num_sms, slots);
+    if (err != cudaSuccess) return err;
+    a.chunks = (a.K + kChunkK - 1) / kChunkK;
+    const Fp4Split sp = fp4_split((uint64_t(a.N) + 15) / 16, a.chunks, (a.T + 7) / 8, B::kMaxWarps, slots);
+    const uint32_t rows = sp.w / sp.ks * 16, tiles = (a.N + rows - 1) / rows;
+    return launch_cluster(kernel, dim3(tiles * sp.c), dim3(sp.w * kWarp), sp.c, B::kSmem, stream, a,
+                          int(sp.ks), sp.c);
 }
 
 template <int F>
 cudaError_t launch_f(const GemvArgs& a, int num_sms, cudaStream_t stream) {
-    const bool wide = a.N >= 32u * 2u * uint32_t(num_sms);
-    if (a.T <= 8) return wide ? launch_r<F, 2, 1>(a, num_sms, stream) : launch_r<F, 1, 1>(a, num_sms, stream);
-    if (a.T <= 16) return wide ? launch_r<F, 2, 2>(a, num_sms, stream) : launch_r<F, 1, 2>(a, num_sms, stream);
-    return wide ? launch_r<F, 2, 4>(a, num_sms, stream) : launch_r<F, 1, 4>(a, num_sms, stream);
+    if (a.T <= 8) return launch_ng<F, 1>(a, num_sms, stream);
+    if (a.T <= 16) return launch_ng<F, 2>(a, num_sms, stream);
+    return launch_ng<F, 4>(a, num_sms, stream);
 }
 
 }  // namespace
