@@ -58,13 +58,14 @@ constexpr uint32_t kChunkK = 512;   // k per chunk
 constexpr uint32_t kUnits = 88;                       // (group, step) units of x that shared memory holds
 constexpr uint32_t kUnit = 2048;                      // one unit: 8 tokens x 128 k, f16
 constexpr uint32_t kInvAt = kUnits * kUnit;           // the units' inverse powers of two, 8 each
-constexpr uint32_t kPartAt = kInvAt + kUnits * 32u;   // partial sums: [warp][8 NG tokens][16 rows]
+constexpr uint32_t kPartAt = kInvAt + kUnits * 32u;   // partial sums: [warp][tokens][16 rows]
 
 template <int F, int NG>
 struct Fp4Block {
     static constexpr int kMaxWarps = NG == 1 ? (F == kWNvfp4 ? MOE_FP4_WNV : MOE_FP4_WMX) : 16;
     static constexpr int kMaxThreads = kMaxWarps * kWarp;
-    static constexpr uint32_t kSmem = kPartAt + kMaxWarps * NG * 512u;
+    // partial sums of up to 32 tokens (8 if NG == 1)
+    static constexpr uint32_t kSmem = kPartAt + kMaxWarps * (NG == 1 ? 512u : 2048u);
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -142,11 +143,12 @@ __device__ __forceinline__ void stage_unit(uint8_t* smem, uint32_t to, const uin
 }
 
 // One lane's weights of a chunk: 64 bytes of its rows g and g + 8 of a tile,
-// and their scales as stored (4 E8M0 or 8 E4M3 bytes).
+// and their scales as loaded: two parts of two granules each (nothing is put
+// together before it is used, as that would wait for the load).
 template <int F>
 struct WChunk4 {
-    Bits<32> w[2][2];                        // [row half][half of the 64 bytes]
-    uint32_t s[2][F == kWNvfp4 ? 2 : 1];
+    Bits<32> w[2][2];        // [row half][half of the 64 bytes]
+    uint32_t s[2][2];        // [row half][part]: 2 E8M0 or 4 E4M3 bytes
 };
 
 // Where a lane's rows lie: its 64 bytes of row g in chunk 0, their scales, and
@@ -160,7 +162,7 @@ struct Shape4 {
     uint64_t half_w, half_s;
     uint32_t rb;         // bytes of a row
     uint32_t whole;      // chunks that lie wholly in a row, if rows may be read in 32-byte pieces (else 0)
-    int scale_align;     // bytes: at most those of a lane's scales (4 or 8)
+    int scale_align;     // bytes: at most 8
 };
 
 template <int F>
@@ -168,76 +170,45 @@ __device__ __forceinline__ Shape4 fp4_shape(uint64_t half_rows, uint32_t K, cons
     const uint32_t rb = row_bytes<F>(K), rs = row_scales<F>(K);
     const uint32_t al = rs & (0u - rs);   // largest power of two that divides a row's scales
     const bool wide = rb % 32u == 0u && reinterpret_cast<uintptr_t>(w) % 32u == 0u;
-    return {half_rows * rb, half_rows * rs, rb, wide ? rb / 256u : 0u, int(min(al, F == kWNvfp4 ? 8u : 4u))};
-}
-
-// This lane's granules of chunk c that lie in the row.
-__device__ __forceinline__ uint32_t granules4(const Shape4& sh, uint32_t c) {
-    const uint32_t at = c * 256u + (threadIdx.x % 4) * 64u;
-    return at < sh.rb ? min((sh.rb - at) / 16u, 4u) : 0u;
-}
-
-// Half `half` (32 bytes per row) of chunk c, at p.w. `whole`: nothing of it is
-// cut off by the end of the row or of the matrix (nearly always), and rows may
-// be read in 32-byte pieces.
-template <int F>
-__device__ __forceinline__ void load_half(WChunk4<F>& a, int half, const Place4& p, const Shape4& sh, uint32_t c, bool whole) {
-    if (whole) {
-        ld_stream(a.w[0][half], p.w + half * 32);
-        ld_stream(a.w[1][half], p.w + sh.half_w + half * 32);
-        return;
-    }
-    const uint32_t n = granules4(sh, c);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            Bits<16> v;
-            if (((p.rows >> h) & 1u) && uint32_t(2 * half + i) < n) ld_stream(v, p.w + h * sh.half_w + half * 32 + i * 16);
-            else v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0u;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) a.w[h][half].w[4 * i + z] = v.w[z];
-        }
+    return {half_rows * rb, half_rows * rs, rb, wide ? rb / 256u : 0u, int(min(al, 8u))};
 }
 
 template <int F>
 __device__ __forceinline__ void load_scales(WChunk4<F>& a, const Place4& at, const Shape4& sh, uint32_t c, bool whole) {
+    constexpr int kPart = F == kWNvfp4 ? 4 : 2;   // bytes of a part
+    const uint32_t n = whole ? 4u : row_granules(sh.rb, c);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint8_t* p = at.s + h * sh.half_s;
-        if (!whole) {
-            const uint32_t n = (at.rows >> h) & 1u ? granules4(sh, c) : 0u;
-            a.s[h][0] = 0u;
-            if constexpr (F == kWNvfp4) a.s[h][1] = 0u;
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-                if (i < n) {
-                    if constexpr (F == kWNvfp4) a.s[h][i / 2] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
-                    else a.s[h][0] |= uint32_t(__ldg(p + i)) << (8 * i);
-                }
-            continue;
-        }
-        if constexpr (F == kWNvfp4) {
-            if (sh.scale_align == 8) {
+        const uint32_t m = whole || ((at.rows >> h) & 1u) ? n : 0u;
+        if (sh.scale_align >= kPart) {
+            if (whole && F == kWNvfp4 && sh.scale_align == 2 * kPart) {
                 const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
                 a.s[h][0] = t.x;
                 a.s[h][1] = t.y;
-            } else if (sh.scale_align == 4) {
-                a.s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-                a.s[h][1] = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
             } else {
-                const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
-                a.s[h][0] = __ldg(v) | uint32_t(__ldg(v + 1)) << 16;
-                a.s[h][1] = __ldg(v + 2) | uint32_t(__ldg(v + 3)) << 16;
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i) {
+                    a.s[h][i] = 0u;
+                    if (m >= 2 * i + 2) {
+                        if constexpr (F == kWNvfp4) a.s[h][i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+                        else a.s[h][i] = __ldg(reinterpret_cast<const uint16_t*>(p) + i);
+                    } else if (m == 2 * i + 1) {
+                        if constexpr (F == kWNvfp4) a.s[h][i] = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i);
+                        else a.s[h][i] = __ldg(p + 2 * i);
+                    }
+                }
             }
-        } else {
-            if (sh.scale_align == 4) {
-                a.s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            } else if (sh.scale_align == 2) {
-                const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
-                a.s[h][0] = __ldg(v) | uint32_t(__ldg(v + 1)) << 16;
-            } else {
-                a.s[h][0] = __ldg(p) | uint32_t(__ldg(p + 1)) << 8 | uint32_t(__ldg(p + 2)) << 16 | uint32_t(__ldg(p + 3)) << 24;
+        } else {   // rows of scales at odd places: granule by granule
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                a.s[h][i] = 0u;
+#pragma unroll
+                for (uint32_t k = 0; k < 2; ++k)
+                    if (2 * i + k < m) {
+                        if constexpr (F == kWNvfp4) a.s[h][i] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + k)) << (16 * k);
+                        else a.s[h][i] |= uint32_t(__ldg(p + 2 * i + k)) << (8 * k);
+                    }
             }
         }
     }
@@ -289,23 +260,25 @@ static __device__ __noinline__ void mxfp4_apart(float* acc, const uint32_t* w, c
 __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole) {
     uint32_t top = 0, low = 255u;
     if (!whole) {
-        const uint32_t n = granules4(sh, c);
+        const uint32_t n = row_granules(sh.rb, c);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, (a.s[h][0] >> (8 * i)) & 255u);
+            for (int i = 0; i < 4; ++i) top = max(top, (a.s[h][i / 2] >> (8 * (i % 2))) & 255u);
         top = __reduce_max_sync(kFull, top);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t m = (p.rows >> h) & 1u ? n : 0u, in = m == 4u ? ~0u : (1u << (8u * m)) - 1u;
-            a.s[h][0] |= top * 0x01010101u & ~in;
+            const uint32_t m = (p.rows >> h) & 1u ? n : 0u;
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i)
+                a.s[h][i] |= m >= 2 * i + 2 ? 0u : m == 2 * i + 1 ? top << 8 : top * 0x0101u;
         }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t x = __byte_perm(a.s[h][0], 0, 0x4440 + i);
+            const uint32_t x = __byte_perm(a.s[h][i / 2], 0, 0x4440 + i % 2);
             top = max(top, x);
             low = min(low, x);
         }
@@ -319,7 +292,7 @@ __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, 
 // that unit's inverse powers of two of the lane's two tokens in C, 2 q and 2 q
 // + 1; f multiplies the sums, top and apart as of mxfp4_top.
 template <int F, int NG>
-__device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& a, const uint32_t (&sc)[2][F == kWNvfp4 ? 2 : 1],
+__device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& a, const uint32_t (&sc)[2][2],
                                          int i, const uint32_t (&xb)[NG], const float* (&inv)[NG], int groups, float f,
                                          uint32_t top, bool apart) {
     uint32_t s[2][2];   // f16 scale in both halves: [row g or g + 8][k 0..15 or 16..31 of the granule]
@@ -342,7 +315,7 @@ __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& 
                 uint32_t w[2][4], x[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    x[h] = (sc[h][0] >> (8 * i)) & 255u;
+                    x[h] = (sc[h][i / 2] >> (8 * (i % 2))) & 255u;
 #pragma unroll
                     for (int z = 0; z < 4; ++z) w[h][z] = a.w[h][i / 2].w[(i % 2) * 4 + z];
                 }
@@ -357,7 +330,7 @@ __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& 
         f *= mxfp4_unit(top);
         const uint32_t shift = (28u - top) * 0x04000400u;   // biased f16 exponent X - top + 28, in both halves
 #pragma unroll
-        for (int k = 0; k < 2; ++k) s[k][0] = s[k][1] = __byte_perm(sc[k][0], 0, 0x4440 + i) * 0x04000400u + shift;
+        for (int k = 0; k < 2; ++k) s[k][0] = s[k][1] = __byte_perm(sc[k][i / 2], 0, 0x4440 + i % 2) * 0x04000400u + shift;
     }
     float c[NG][4] = {};
 #pragma unroll
@@ -404,29 +377,29 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Sh
     p.w += c0 * 256u;
     p.s += c0 * (kChunkK / WInfo<F>::kBlock);
     WChunk4<F> a;
-    load_half(a, 0, p, sh, c0, c0 < whole);
-    load_half(a, 1, p, sh, c0, c0 < whole);
+    load_rows(a.w, 0, p.w, sh.half_w, c0 < whole, p.rows, row_granules(sh.rb, c0), sh.whole > 0u);
+    load_rows(a.w, 1, p.w, sh.half_w, c0 < whole, p.rows, row_granules(sh.rb, c0), sh.whole > 0u);
     load_scales(a, p, sh, c0, c0 < whole);
 #pragma unroll 1
     for (uint32_t c = c0; c < c1; ++c) {
         uint32_t top = 0;
         bool apart = false;
         if constexpr (F == kWMxfp4) top = mxfp4_top(a, apart, p, sh, c, c < whole);
-        uint32_t sc[2][F == kWNvfp4 ? 2 : 1];
+        uint32_t sc[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int z = 0; z < (F == kWNvfp4 ? 2 : 1); ++z) sc[h][z] = a.s[h][z];
+            for (int z = 0; z < 2; ++z) sc[h][z] = a.s[h][z];
         const bool more = c + 1 < c1;
         p.w += 256;
         p.s += kChunkK / WInfo<F>::kBlock;
         if (more) load_scales(a, p, sh, c + 1, c + 1 < whole);
         fp4_step<F, NG>(acc, a, sc, 0, xb, inv, groups, f, top, apart);
         fp4_step<F, NG>(acc, a, sc, 1, xb, inv, groups, f, top, apart);
-        if (more) load_half(a, 0, p, sh, c + 1, c + 1 < whole);
+        if (more) load_rows(a.w, 0, p.w, sh.half_w, c + 1 < whole, p.rows, row_granules(sh.rb, c + 1), sh.whole > 0u);
         fp4_step<F, NG>(acc, a, sc, 2, xb, inv, groups, f, top, apart);
         fp4_step<F, NG>(acc, a, sc, 3, xb, inv, groups, f, top, apart);
-        if (more) load_half(a, 1, p, sh, c + 1, c + 1 < whole);
+        if (more) load_rows(a.w, 1, p.w, sh.half_w, c + 1 < whole, p.rows, row_granules(sh.rb, c + 1), sh.whole > 0u);
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             xb[n] += 4 * kUnit;
@@ -434,72 +407,6 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Sh
         }
     }
 }
-
-// Barrier of the KS warps of row group rg.
-__device__ __forceinline__ void group_sync(int rg, int KS) {
-    if (KS == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(rg + 1), "r"(KS * kWarp) : "memory");
-}
-
-// One group's accumulators -> [token][row], 16 rows.
-template <int NG>
-__device__ __forceinline__ void store_group(float* p, const float (&acc)[NG][4], int n) {
-    const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
-#pragma unroll
-    for (int k = 0; k < NG; ++k)
-        if (k == n) {
-#pragma unroll
-            for (int z = 0; z < 4; ++z) p[(2 * q + (z & 1)) * 16 + g + (z >> 1) * 8] = acc[k][z];
-        }
-}
-
-// Sum over the KS splits of k (warps rg KS ..) of element i of their `stride`
-// floats.
-__device__ __forceinline__ float sum_splits(const float* s_part, int rg, int KS, int stride, int i) {
-    const float* p = s_part + rg * KS * stride + i;
-    float v = p[0];
-    for (int k = 1; k < KS; ++k) v += p[k * stride];
-    return v;
-}
-
-// Clusters of C blocks (C = 1 .. 8) of a kernel that one device holds at once,
-// asked once per device: with one block per SM and the SMs of a graphics
-// cluster in odd numbers, far fewer than SMs / C (a GEMV in clusters of 7 ran
-// in three waves).
-struct ClusterSlots {
-    std::atomic<uint64_t> known[64] = {};   // per device: 8 bytes, min(slots, 255)
-
-    template <typename Kernel>
-    cudaError_t get(Kernel kernel, uint32_t threads, size_t smem, int num_sms, uint32_t (&slots)[9]) {
-        int dev = 0;
-        cudaError_t err = cudaGetDevice(&dev);
-        if (err != cudaSuccess) return err;
-        uint64_t v = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-        if (v == 0) {
-            for (uint32_t c = 1; c <= 8; ++c) {
-                cudaLaunchConfig_t cfg = {};
-                cfg.gridDim = dim3(c * 8);
-                cfg.blockDim = dim3(threads);
-                cfg.dynamicSmemBytes = smem;
-                cudaLaunchAttribute attr[1];
-                attr[0].id = cudaLaunchAttributeClusterDimension;
-                attr[0].val.clusterDim.x = c;
-                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-                cfg.attrs = attr;
-                cfg.numAttrs = 1;
-                int n = num_sms;
-                if (c > 1) {
-                    err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-                    if (err != cudaSuccess) return err;
-                }
-                v |= uint64_t(std::max(1, std::min(n, 255))) << (8 * (c - 1));
-            }
-            if (dev < 64) known[dev].store(v, std::memory_order_relaxed);
-        }
-        for (uint32_t c = 1; c <= 8; ++c) slots[c] = uint32_t(v >> (8 * (c - 1))) & 255u;
-        return cudaSuccess;
-    }
-};
 
 // How a kernel of one block per SM over `tiles` row tiles divides its work: W
 // warps per block, KS splits of k in a block, C blocks of a cluster, that share
@@ -529,25 +436,6 @@ inline Fp4Split fp4_split(uint64_t tiles, uint32_t chunks, uint32_t groups, uint
             }
         }
     return best;
-}
-
-// s_sum[T][rows] summed over the C blocks of the cluster, in rank order, to
-// store(t, row, value).
-template <typename Store>
-__device__ __forceinline__ void cluster_store(const float* s_sum, int total, int rows, uint32_t rank, uint32_t C, Store&& store) {
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-    for (int o = int(threadIdx.x + rank * blockDim.x); o < total; o += int(blockDim.x * C)) {
-        float v;
-        if (C > 1) {
-            v = ld_cluster(s_sum + o, 0);
-            for (uint32_t c = 1; c < C; ++c) v += ld_cluster(s_sum + o, c);
-        } else {
-            v = s_sum[o];
-        }
-        store(o / rows, o % rows, v);
-    }
-    if (C > 1) cluster_sync();   // the others may still read this block's sums
 }
 
 }  // namespace moe

@@ -88,6 +88,4 @@ __device__ __forceinline__ void route_few(const LayerArgs& a, FewRoute& s, bool 
     __syncthreads();
 }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
-
 }  // namespace moe

@@ -11,15 +11,17 @@
 // plain sum over the concatenated k of all chosen experts, in float32.
 //
 // Routing is redundant: every block routes the whole batch in shared memory
-// (tens of KB of logits at most), so no block waits for another.
-//   fc1: an item is 8 R columns of one expert's activation. A tile's 16 A rows
-//   are 8 gate rows and the same 8 up rows, so one lane's accumulators hold
-//   both halves of a SwiGLU. The block's warps split k; blocks sweep the items
-//   grid-stride. The activation is stored compactly, expert-sorted (row
-//   off[d] + rank of the token among the expert's), for the tokens routed.
-//   fc2: a cluster of C blocks takes 16 R output columns; its warps split the
-//   (expert, k) units of all chosen experts. B columns are the tokens
-//   themselves, zero where a token is not routed to the expert.
+// (tens of KB of logits at most), so no block waits for another. A warp takes
+// tiles of 16 weight rows (few_device.cuh); the KS splits of k of a block sum
+// in shared memory.
+//   fc1: a tile is 8 gate rows and the same 8 up rows, so 8 columns of one
+//        expert's activation; a block takes an even share of all tiles. B
+//        columns are the expert's own tokens. The activation is stored
+//        compactly, expert-sorted (row off[d] + rank of the token).
+//   fc2: a cluster of C blocks takes 16 output columns per row group; its
+//        blocks and their KS splits share the (expert, chunk) list evenly. B
+//        columns are the tokens themselves, zero where a token is not routed to
+//        the expert, so the sums stay in registers to the end.
 // All sums are taken in a fixed order: results do not depend on timing.
 #include "few_device.cuh"
 #include "few_route.cuh"
@@ -29,266 +31,200 @@
 namespace moe {
 namespace {
 
-constexpr int kNw = 8;
+constexpr int kNw = 8;             // warps per block
 constexpr int kNt = kNw * kWarp;
-constexpr int kDepth = 2;                         // chunks in flight per warp
-// fc1: the block's chunks are numbered item by item; a warp takes chunk
-// u = warp, warp + kNw, ... of every item, `per` of them (the last may lie
-// outside), so that its ring runs on across items.
-template <int R, int NG, int US>
-__global__ void __launch_bounds__(kNt, 2) fc1_kernel(LayerArgs a) {
-    using Ring = WRing<kWBf16, R, US, kDepth>;
-    extern __shared__ __align__(16) uint8_t smem[];
+constexpr uint32_t kChunk = 128;   // k per chunk
+
+// The products of half a chunk (64 k) with one group of tokens.
+__device__ __forceinline__ void mma_half(float (&c)[4], const Bits<32>& w0, const Bits<32>& w1, const uint4& x0, const uint4& x1) {
+    const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(w0.w[2 * j]), "r"(w1.w[2 * j]), "r"(w0.w[2 * j + 1]), "r"(w1.w[2 * j + 1]), "r"(b[2 * j]), "r"(b[2 * j + 1]));
+}
+
+// Half of a lane's 64 bytes of x in chunk c (NULL: zeros).
+__device__ __forceinline__ void load_x(uint4 (&x)[2], const uint16_t* row, uint32_t K, uint32_t c, int half) {
+    const uint32_t k0 = c * kChunk + (threadIdx.x % 4) * 32u + half * 16u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row != nullptr && k0 + i * 8u < K) x[i] = __ldg(reinterpret_cast<const uint4*>(row + k0) + i);
+    }
+}
+
+// Where a lane's rows lie: its 64 bytes of row g in chunk 0, the distance to
+// row g + 8, and which of the two exist.
+struct Rows {
+    const uint8_t* w;
+    uint64_t half_w;
+    uint32_t rows;
+};
+
+// The chunks c0 .. c1 - 1 of one tile of rows of K values, against the groups of
+// 8 tokens set in `live` (the same for the whole warp); x[n]: this lane's
+// token's row of group n, or NULL. The next chunk's loads go out as soon as
+// half of the registers is used up.
+template <int NG>
+__device__ __forceinline__ void bf16_tile(float (&acc)[NG][4], Rows p, uint32_t K, bool wide, uint32_t c0, uint32_t c1,
+                                          const uint16_t* const (&x)[NG], uint32_t live) {
+    if (c0 >= c1) return;
+    const uint32_t rb = 2 * K, whole = wide && __all_sync(kFull, p.rows == 3u) ? rb / 256u : 0u;   // chunks below it are whole
+    Bits<32> w[2][2];
+    p.w += c0 * 256u;
+    load_rows(w, 0, p.w, p.half_w, c0 < whole, p.rows, row_granules(rb, c0), wide);
+    load_rows(w, 1, p.w, p.half_w, c0 < whole, p.rows, row_granules(rb, c0), wide);
+#pragma unroll 1
+    for (uint32_t c = c0; c < c1; ++c) {
+        p.w += 256;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                if (NG > 1 && !((live >> n) & 1u)) continue;
+                uint4 b[2];
+                load_x(b, x[n], K, c, half);
+                mma_half(acc[n], w[0][half], w[1][half], b[0], b[1]);
+            }
+            if (c + 1 < c1) load_rows(w, half, p.w, p.half_w, c + 1 < whole, p.rows, row_granules(rb, c + 1), wide);
+        }
+    }
+}
+
+__device__ __forceinline__ bool rows_wide(uint32_t K, const void* w) {
+    return K % 16 == 0 && reinterpret_cast<uintptr_t>(w) % 32 == 0;
+}
+
+template <int NG>
+__global__ void __launch_bounds__(kNt, NG == 4 ? 2 : 3) fc1_kernel(LayerArgs a, int KS) {
     __shared__ FewRoute s;
+    __shared__ float s_part[kNw * 128];          // [warp][8 tokens][16 rows]
     pdl_wait_and_release();
     route_few(a, s, blockIdx.x == 0);
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, q = lane % 4;
-    const uint32_t K = uint32_t(a.H), I = uint32_t(a.I);
-    const uint32_t rb = row_bytes<kWBf16>(K);
-    const uint32_t tiles = (I + 8 * R - 1) / (8 * R);
-    const uint32_t per = ((rb + 63) / 64 + US * kNw - 1) / (US * kNw);
-    const uint32_t items = uint32_t(s.nd) * tiles;
-    const int out_n = a.T * 16 * R;
-    float* s_red = reinterpret_cast<float*>(smem + kNw * Ring::kBytes);   // [kNw][T][16 R]
-    const uint8_t* w13 = static_cast<const uint8_t*>(a.w13);
-    const WStride st = {8ull * rb, uint64_t(I) * rb, 0, 0};
-
-    // the chunk of (item, i-th of this warp's)
-    struct Cursor {
-        uint32_t item, i;
-        WChunk c;
-    };
-    auto place = [&](Cursor& x) {   // rows of x.item
-        x.c.rows = 0;
-        if (x.item < items) {
-            const uint32_t d = x.item / tiles, j = (x.item - d * tiles) * (8 * R) + g;
-            const uint64_t row = uint64_t(s.expert[d]) * 2 * I + j;
-            x.c.w = w13 + row * rb + q * 16;
+    const int RG = kNw / KS, rg = warp / KS, ks = warp % KS;
+    const uint32_t H = uint32_t(a.H), I = uint32_t(a.I), tiles = I / 8, chunks = (H + kChunk - 1) / kChunk;
+    const uint32_t total = uint32_t(s.nd) * tiles, k0 = chunks * ks / KS, k1 = chunks * (ks + 1) / KS;
+    const uint32_t begin = uint32_t(uint64_t(total) * blockIdx.x / gridDim.x), end = uint32_t(uint64_t(total) * (blockIdx.x + 1) / gridDim.x);
+    const bool wide = rows_wide(H, a.w13);
+    for (uint32_t t = begin + rg; t < end; t += RG) {
+        const uint32_t d = t / tiles, j0 = (t - d * tiles) * 8;
+        const int m = __popc(s.tokens[d]), groups = (m + 7) / 8;
+        const uint16_t* x[NG];
 #pragma unroll
-            for (int r = 0; r < R; ++r) x.c.rows |= (j + 8 * r < I ? 3u : 0u) << (2 * r);
-        }
-    };
-    auto step = [&](Cursor& x) { x.c.step = (x.i * kNw + warp) * US; };
-    auto advance = [&](Cursor& x) {
-        if (++x.i == per) {
-            x.i = 0;
-            x.item += gridDim.x;
-            place(x);
-        }
-        step(x);
-    };
-
-    Ring ring;
-    ring.init(smem + warp * Ring::kBytes);
-    Cursor fw = {blockIdx.x, 0, {w13, nullptr, 0, 0}};   // fetch cursor of the weights, kDepth chunks ahead
-    place(fw);
-    step(fw);
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-        ring.fetch(i * Ring::kChunk, fw.c, st, w13, rb);
-        Ring::commit();
-        advance(fw);
-    }
-    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const uint32_t d = item / tiles, j0 = (item - d * tiles) * (8 * R);
-        const uint32_t tokens = s.tokens[d];
-        const int m = __popc(tokens), groups = (m + 7) / 8;
-        const uint16_t* xrow[NG];
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-            xrow[n] = n * 8 + g < m ? a.x + uint64_t(s.row_t[s.off[d] + n * 8 + g]) * K : nullptr;
-        float acc[R][NG][4] = {};
-        for (uint32_t i = 0; i < per; ++i) {
-            const uint32_t s0 = (i * kNw + warp) * US;
-            BGran<kWBf16> b0[US];
-#pragma unroll
-            for (int k = 0; k < US; ++k) load_x<kWBf16>(b0[k], xrow[0], xrow[0] != nullptr, s0 + k, q, K);
-            Ring::wait();
-            if (s0 * 64u < rb) {
-#pragma unroll
-                for (int k = 0; k < US; ++k)
-                    bf16_step<R, NG>(acc, (1u << groups) - 1u,
-                                       [&](AGran& w, int r) { ring.read(w, k, r); },
-                                       [&](int n, BGran<kWBf16>& b) {
-                                           if (n == 0) b = b0[k];
-                                           else load_x<kWBf16>(b, xrow[n], xrow[n] != nullptr, s0 + k, q, K);
-                                       });
+        for (int n = 0; n < NG; ++n) x[n] = n * 8 + g < m ? a.x + uint64_t(s.row_t[s.off[d] + n * 8 + g]) * H : nullptr;
+        const Rows p = {static_cast<const uint8_t*>(a.w13) + (uint64_t(s.expert[d]) * 2 * I + j0 + g) * (2 * H) + q * 64,
+                        uint64_t(I) * (2 * H), 3u};
+        float acc[NG][4] = {};
+        bf16_tile<NG>(acc, p, H, wide, k0, k1, x, (1u << groups) - 1u);
+        for (int n = 0; n < groups; ++n) {
+            group_sync(rg, KS);
+            store_group<NG>(s_part + warp * 128, acc, n);
+            group_sync(rg, KS);
+            // (token, column): gate and up rows lie 8 apart
+            for (int o = threadIdx.x % (KS * kWarp); o < 64; o += KS * kWarp) {
+                const int c = o / 8;
+                if (n * 8 + c >= m) continue;
+                const uint32_t row = s.off[d] + n * 8 + c;
+                const float gate = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8), up = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8 + 8);
+                a.act[uint64_t(row) * I + j0 + o % 8] = uint16_t(pack_bf16x2(s.row_w[row] * (silu(gate) * up), 0.0f));
             }
-            __syncwarp();   // the slot is read: refill it
-            ring.fetch(ring.slot, fw.c, st, w13, rb);
-            Ring::commit();
-            ring.next();
-            advance(fw);
         }
-        store_partial<R, NG>(s_red + warp * out_n, acc, m);
-        __syncthreads();
-        // thread -> (token of the expert, column); the two halves lie 8 rows apart
-        for (int o = threadIdx.x; o < m * 8 * R; o += kNt) {
-            const int c = o / (8 * R), i = o % (8 * R);
-            const int at = c * (16 * R) + (i / 8) * 16 + i % 8;
-            float gate = 0.0f, up = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kNw; ++w) {
-                gate += s_red[w * out_n + at];
-                up += s_red[w * out_n + at + 8];
-            }
-            const uint32_t row = s.off[d] + c;
-            if (j0 + i < I) a.act[uint64_t(row) * I + j0 + i] = uint16_t(pack_bf16x2(s.row_w[row] * (silu(gate) * up), 0.0f));
-        }
-        __syncthreads();
     }
-    Ring::drain();
 }
 
-// fc2: the chunks of all chosen experts, in order, are dealt to the warps of
-// the cluster.
-template <int R, int NG, int US>
-__global__ void __launch_bounds__(kNt, 2) fc2_kernel(LayerArgs a, uint32_t C) {
-    using Ring = WRing<kWBf16, R, US, kDepth>;
-    extern __shared__ __align__(16) uint8_t smem[];
+template <int NG>
+__global__ void __launch_bounds__(kNt, NG == 4 ? 2 : 3) fc2_kernel(LayerArgs a, int KS, uint32_t C) {
     __shared__ FewRoute s;
+    __shared__ float s_part[kNw * 128];
+    __shared__ float s_sum[kMaxTokens * kNw * 16];   // [T][rows]
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, q = lane % 4;
-    const uint32_t K = uint32_t(a.I), H = uint32_t(a.H);
-    const uint32_t rb = row_bytes<kWBf16>(K);
-    const uint32_t rank = blockIdx.x % C, row0 = blockIdx.x / C * (16 * R);
-    const uint32_t chunks = ((rb + 63) / 64 + US - 1) / US;   // per expert
-    const int out_n = a.T * 16 * R;
-    float* s_red = reinterpret_cast<float*>(smem + kNw * Ring::kBytes);   // [kNw][T][16 R]
-    float* s_warp = s_red + warp * out_n;
-    // Before the wait for fc1: routing from the logits and the first weights.
-    // Neither is written by fc1, and fc1 let this kernel start only after its
-    // own wait, so whatever wrote them has completed.
+    const int RG = kNw / KS, rg = warp / KS, ks = warp % KS, rows = RG * 16;
+    const uint32_t H = uint32_t(a.H), I = uint32_t(a.I), chunks = (I + kChunk - 1) / kChunk;
+    const uint32_t rank = blockIdx.x % C, row0 = blockIdx.x / C * rows, mine = row0 + rg * 16 + g;
+    // Before the wait for fc1: routing from the logits. They are not written by
+    // fc1, and fc1 let this kernel start only after its own wait, so whatever
+    // wrote them has completed.
     route_few(a, s, false);
-    const uint8_t* w2 = static_cast<const uint8_t*>(a.w2);
-    const WStride st = {16ull * rb, 8ull * rb, 0, 0};
-    uint32_t rows = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * R; ++i) rows |= uint32_t(row0 + 8 * i + g < H) << i;
-    const uint32_t nd = uint32_t(s.nd), stride = C * kNw, sd = stride / chunks, su = stride - sd * chunks;
-    struct Cursor {
-        uint32_t d, u;
-        WChunk c;
-    };
-    auto place = [&](Cursor& x) {
-        x.c.rows = 0;
-        if (x.d < nd) {
-            const uint64_t row = uint64_t(s.expert[x.d]) * H + row0 + g;
-            x.c.w = w2 + row * rb + q * 16;
-            x.c.rows = rows;
-        }
-        x.c.step = x.u * US;
-    };
-    auto advance = [&](Cursor& x) {
-        x.u += su;
-        x.d += sd;
-        if (x.u >= chunks) {
-            x.u -= chunks;
-            ++x.d;
-        }
-        place(x);
-    };
-    Ring ring;
-    ring.init(smem + warp * Ring::kBytes);
-    const uint32_t first = rank * kNw + warp;
-    Cursor fw = {first / chunks, first % chunks, {w2, nullptr, 0, 0}};
-    place(fw);
-    Cursor cur = fw;
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-        ring.fetch(i * Ring::kChunk, fw.c, st, w2, rb);
-        Ring::commit();
-        advance(fw);
-    }
     pdl_wait_and_release();
-
-    float acc[R][NG][4] = {};
-    while (cur.d < nd) {
-        const uint32_t d = cur.d, s0 = cur.u * US;
-        const uint32_t tokens = s.tokens[d], off = s.off[d];
-        const int m = __popc(tokens);
-        auto load = [&](int n, int k, BGran<kWBf16>& b) {
-            const uint32_t c = n * 8 + g;   // column: token c
-            const bool mine = (tokens >> c) & 1u;
-            const uint32_t row = off + __popc(tokens & ((1u << c) - 1u));
-            load_x<kWBf16>(b, a.act + uint64_t(row) * K, mine, s0 + k, q, K);
-        };
-        uint32_t live = 0;   // groups with a token of this expert: warp-uniform
+    const bool wide = rows_wide(I, a.w2);
+    const uint32_t rows_ok = uint32_t(mine < H) | uint32_t(mine + 8 < H) << 1;
+    // this warp's part of the (expert, chunk) list
+    const uint64_t all = uint64_t(s.nd) * chunks, slot = rank * KS + ks, slots = uint64_t(C) * KS;
+    const uint32_t stop = uint32_t(all * (slot + 1) / slots);
+    float acc[NG][4] = {};
+    for (uint32_t c = uint32_t(all * slot / slots); c < stop;) {
+        const uint32_t d = c / chunks, k0 = c - d * chunks, k1 = min(chunks, k0 + (stop - c)), m = s.tokens[d];
+        const uint16_t* x[NG];
+        uint32_t live = 0;
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-            live |= uint32_t(((tokens >> (8 * n)) & 0xffu) != 0u) << n;
-        BGran<kWBf16> b0[US];
-        if (live & 1u) {
-#pragma unroll
-            for (int k = 0; k < US; ++k) load(0, k, b0[k]);
+        for (int n = 0; n < NG; ++n) {
+            const uint32_t t = n * 8 + g;
+            x[n] = (m >> t) & 1u ? a.act + uint64_t(s.off[d] + __popc(m & ((1u << t) - 1u))) * I : nullptr;
+            live |= uint32_t(((m >> (8 * n)) & 0xffu) != 0u) << n;
         }
-        Ring::wait();
-#pragma unroll
-        for (int k = 0; k < US; ++k)
-            bf16_step<R, NG>(acc, live, [&](AGran& w, int r) { ring.read(w, k, r); },
-                               [&](int n, BGran<kWBf16>& b) {
-                                   if (n == 0) b = b0[k];
-                                   else load(n, k, b);
-                               });
-        __syncwarp();   // the slot is read: refill it
-        ring.fetch(ring.slot, fw.c, st, w2, rb);
-        Ring::commit();
-        ring.next();
-        advance(fw);
-        advance(cur);
+        const Rows p = {static_cast<const uint8_t*>(a.w2) + (uint64_t(s.expert[d]) * H + mine) * (2 * I) + q * 64, 8ull * (2 * I), rows_ok};
+        bf16_tile<NG>(acc, p, I, wide, k0, k1, x, live);
+        c += k1 - k0;
     }
-    Ring::drain();
-    store_partial<R, NG>(s_warp, acc, a.T);
-    __syncthreads();
-    if (C > 1) {
-        for (int o = threadIdx.x; o < out_n; o += kNt) {
-            float v = s_red[o];
-#pragma unroll
-            for (int w = 1; w < kNw; ++w) v += s_red[w * out_n + o];
-            s_red[o] = v;   // this thread alone reads and writes column o
-        }
-        cluster_sync();
+    for (int n = 0; n < (a.T + 7) / 8; ++n) {
+        __syncthreads();
+        store_group<NG>(s_part + warp * 128, acc, n);
+        __syncthreads();
+        for (int o = threadIdx.x; o < 8 * rows; o += kNt)
+            if (n * 8 + o / rows < a.T) s_sum[(n * 8 + o / rows) * rows + o % rows] = sum_splits(s_part, o % rows / 16, KS, 128, o / rows * 16 + o % 16);
     }
-    for (int o = threadIdx.x + (C > 1 ? int(rank) * kNt : 0); o < out_n; o += kNt * int(C)) {
-        float v;
-        if (C > 1) {
-            v = ld_cluster(s_red + o, 0);
-            for (uint32_t c = 1; c < C; ++c) v += ld_cluster(s_red + o, c);
-        } else {
-            v = s_red[o];
-#pragma unroll
-            for (int w = 1; w < kNw; ++w) v += s_red[w * out_n + o];
-        }
-        const uint32_t t = uint32_t(o) / (16 * R), row = row0 + uint32_t(o) % (16 * R);
-        if (row < H) a.out[uint64_t(t) * H + row] = uint16_t(pack_bf16x2(v, 0.0f));
-    }
-    if (C > 1) cluster_sync();   // the others may still read this block's sums
+    cluster_store(s_sum, a.T * rows, rows, rank, C, [&](int t, int i, float v) {
+        if (row0 + i < H) a.out[uint64_t(t) * H + row0 + i] = uint16_t(pack_bf16x2(v, 0.0f));
+    });
 }
 
-template <int R, int NG, int US>
-cudaError_t launch_r(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-    auto fc1 = fc1_kernel<R, NG, US>;
-    auto fc2 = fc2_kernel<R, NG, US>;
-    static SmemGrant grant1, grant2;
-    cudaError_t err = grant1.ensure(fc1);
-    if (err == cudaSuccess) err = grant2.ensure(fc2);
+template <int NG>
+cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
+    auto fc1 = fc1_kernel<NG>;
+    auto fc2 = fc2_kernel<NG>;
+    constexpr uint32_t kPerSm = NG == 4 ? 2 : 3;
+    static ClusterSlots clusters;
+    const uint32_t slots1 = kPerSm * uint32_t(num_sms);
+    uint32_t slots[9];
+    cudaError_t err = clusters.get(fc2, kNt, 0, int(slots1), slots);
     if (err != cudaSuccess) return err;
-    const size_t smem = kNw * WRing<kWBf16, R, US, kDepth>::kBytes + sizeof(float) * kNw * a.T * 16 * R;
-    const uint64_t nd = std::min<uint64_t>(a.E, uint64_t(a.T) * a.k);   // most experts that can be chosen
-    const uint64_t items = nd * ((uint64_t(a.I) + 8 * R - 1) / (8 * R));
-    const uint32_t grid = uint32_t(std::min<uint64_t>(items, 2ull * num_sms));
-    err = launch_pdl(fc1, dim3(grid), dim3(kNt), smem, stream, a);
+    // the experts that a batch of independent tokens is expected to choose
+    double miss = 1.0;
+    for (int t = 0; t < a.T; ++t) miss *= 1.0 - double(a.k) / a.E;
+    const double nd = std::max<double>(a.k, a.E * (1.0 - miss));
+    // fc1: splits of k until every warp has about three pieces (the last then costs little)
+    const uint32_t chunks1 = (uint32_t(a.H) + kChunk - 1) / kChunk;
+    const uint64_t tiles1 = uint64_t(nd * (a.I / 8)), most = std::min<uint64_t>(a.E, uint64_t(a.T) * a.k) * uint64_t(a.I / 8);
+    uint32_t ks = 1;
+    while (ks < uint32_t(kNw) && 4 * ks <= chunks1 && tiles1 * ks < 3ull * kNw * slots1) ks *= 2;
+    const uint32_t grid = uint32_t(std::min<uint64_t>((most * ks + kNw - 1) / kNw, slots1));
+    err = launch_pdl(fc1, dim3(grid), dim3(kNt), 0, stream, a, int(ks));
     if (err != cudaSuccess) return err;
-    const uint32_t tiles = (uint32_t(a.H) + 16 * R - 1) / (16 * R);
-    const uint32_t C = split_k(tiles, 2u * uint32_t(num_sms), 8);
-    return launch_cluster(fc2, dim3(tiles * C), dim3(kNt), C, smem, stream, a, C);
+    // fc2: of the splits (KS in a block, C blocks) the one with the fullest waves, then the fewest
+    const uint32_t chunks2 = uint32_t(nd * ((uint32_t(a.I) + kChunk - 1) / kChunk));
+    uint32_t KS = 1, C = 1;
+    double full = -1.0;
+    for (uint32_t k = 1; k <= uint32_t(kNw); k *= 2) {
+        const uint32_t tiles = (uint32_t(a.H) + kNw / k * 16 - 1) / (kNw / k * 16);
+        for (uint32_t c = 1; c <= 8 && (c * k == 1 || 4 * c * k <= chunks2); ++c) {
+            const uint32_t waves = (tiles + slots[c] - 1) / slots[c];
+            const double f = double(tiles) * c / (double(waves) * slots1) - 0.03 * (waves - 1) - (c > 1 ? 0.02 : 0.0);
+            if (f > full + 0.02) { full = f; KS = k; C = c; }
+        }
+    }
+    const uint32_t tiles = (uint32_t(a.H) + kNw / KS * 16 - 1) / (kNw / KS * 16);
+    return launch_cluster(fc2, dim3(tiles * C), dim3(kNt), C, 0, stream, a, int(KS), C);
 }
 
 }  // namespace
 
 cudaError_t launch_layer_bf16(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.T <= 8) return launch_r<1, 1, 4>(a, num_sms, stream);
-    if (a.T <= 16) return launch_r<1, 2, 4>(a, num_sms, stream);
-    return launch_r<1, 4, 4>(a, num_sms, stream);
+    if (a.T <= 8) return launch_ng<1>(a, num_sms, stream);
+    if (a.T <= 16) return launch_ng<2>(a, num_sms, stream);
+    return launch_ng<4>(a, num_sms, stream);
 }
 
 }  // namespace moe

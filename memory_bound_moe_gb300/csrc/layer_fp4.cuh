@@ -1,7 +1,10 @@
 // Kernels of the MoE layer for a few tokens with 4-bit weights, on the inner
 // loop of few_fp4.cuh. See layer_bf16.cu for what fc1 and fc2 compute and how
 // the batch is routed. Up to 8 tokens the B columns are the tokens themselves;
-// above, they are the expert's own tokens, 8 to a group.
+// above, they are the expert's own tokens, 8 to a group and two groups to a
+// pass: an expert with more than 16 of at most 32 tokens takes a second pass
+// over its weights (from L2 or not), which is rare enough that two more groups'
+// accumulators in every warp would cost more.
 //   fc1: a tile is 8 gate rows and the same 8 up rows, so 8 columns of one
 //        expert's activation; a block takes an even share of all tiles, RG at a
 //        time. Up to 8 tokens one converted x serves every expert, and if it
@@ -36,12 +39,12 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
     const uint32_t rs = row_scales<F>(H);
     float* s_part = reinterpret_cast<float*>(smem + kPartAt);
     uint32_t staged = ~0u;   // what x shared memory holds
-    uint32_t stop;
-    for (uint32_t t0 = begin; t0 < end; t0 = min(t0 + RG, stop)) {
+    uint32_t stop, first = 0;   // first: the pass's first token of the expert
+    for (uint32_t t0 = begin; t0 < end;) {
         // the row groups' tiles t0 .. t0 + RG - 1, of one expert if kCompact
         const uint32_t x = kCompact ? t0 / tiles : 0u;
         stop = kCompact ? min(end, (x + 1) * tiles) : end;
-        const int groups = kCompact ? (__popc(s.tokens[x]) + 7) / 8 : 1;
+        const int left = kCompact ? __popc(s.tokens[x]) - int(first) : 8, groups = min(NG, (left + 7) / 8);
         const uint32_t t = t0 + rg, d = min(t, stop - 1u) / tiles, j0 = (t - d * tiles) * 8, e = s.expert[d], m = s.tokens[d];
         const uint64_t row = uint64_t(e) * 2 * I + j0 + g;
         const Place4 p = {static_cast<const uint8_t*>(a.w13) + row * sh.rb + q * 64,
@@ -51,23 +54,30 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
         float acc[NG][4] = {};
         for (uint32_t s0 = 0; s0 < chunks; s0 += slice) {
             const uint32_t n = min(slice, chunks - s0), per = n * 4;
-            if (staged != x * 65536u + s0) {   // at most 2048 chunks
+            if (staged != (x * 4u + first / 8u) * 4096u + s0) {   // s0 < 2048
                 __syncthreads();
                 for (uint32_t u = warp; u < per * groups; u += W) {
                     const uint32_t gr = u / per, c = gr * 8 + g;
                     const uint16_t* xr = nullptr;
                     if (kCompact) {
-                        if (int(c) < __popc(s.tokens[x])) xr = a.x + uint64_t(s.row_t[s.off[x] + c]) * H;
+                        if (int(c) < left) xr = a.x + uint64_t(s.row_t[s.off[x] + first + c]) * H;
                     } else if (int(c) < a.T) {
                         xr = a.x + uint64_t(c) * H;
                     }
                     stage_unit(smem, u, xr, H, s0 + (u - gr * per) / 4, u % 4);
                 }
                 __syncthreads();
-                staged = x * 65536u + s0;
+                staged = (x * 4u + first / 8u) * 4096u + s0;
             }
             const uint32_t k0 = n * ks / KS, k1 = n * (ks + 1) / KS;
             if (t < stop) fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups, f);
+        }
+        // a pass over the block's tiles of the expert, then the next 8 NG tokens or the next expert
+        const uint32_t tokens0 = first;
+        t0 = min(t0 + RG, stop);
+        if (kCompact && t0 == stop) {
+            first = left > 8 * NG ? first + 8 * NG : 0u;
+            if (first > 0u) t0 = max(begin, x * tiles);
         }
         if (t >= stop) continue;   // the whole row group
         for (int n = 0; n < groups; ++n) {
@@ -76,7 +86,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
             group_sync(rg, KS);
             // (token, column): gate and up rows lie 8 apart
             for (int o = threadIdx.x % (KS * kWarp); o < 64; o += KS * kWarp) {
-                const int c = o / 8, col = n * 8 + c;
+                const int c = o / 8, col = int(tokens0) + n * 8 + c;
                 if (kCompact ? col >= __popc(m) : !((m >> col) & 1u)) continue;
                 const uint32_t to = s.off[d] + (kCompact ? col : __popc(m & ((1u << col) - 1u)));
                 const float gate = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8), up = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8 + 8);
@@ -110,18 +120,18 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
     const uint64_t all = uint64_t(s.nd) * chunks;
     const uint32_t c1 = uint32_t(all * (rank + 1) / C);
     float acc[NG][4] = {};
-    uint32_t n;
-    for (uint32_t c0 = uint32_t(all * rank / C); c0 < c1; c0 += n) {
-        // the slice: chunks c0 .. c0 + n - 1 of the list
-        const uint32_t d0 = c0 / chunks, m0 = s.tokens[d0];
-        const int groups = kCompact ? (__popc(m0) + 7) / 8 : 1;
+    uint32_t n, first = 0;   // first: the pass's first token of the expert
+    for (uint32_t c0 = uint32_t(all * rank / C); c0 < c1;) {
+        // the slice: chunks c0 .. c0 + n - 1 of the list, for 8 NG tokens of the expert if kCompact
+        const uint32_t d0 = c0 / chunks;
+        const int left = kCompact ? __popc(s.tokens[d0]) - int(first) : 8, groups = min(NG, (left + 7) / 8);
         n = min(kUnits / 4 / groups, (kCompact ? min(c1, (d0 + 1) * chunks) : c1) - c0);
         const uint32_t per = n * 4;
         __syncthreads();
         for (uint32_t u = warp; u < per * groups; u += W) {
             const uint32_t gr = u / per, c = c0 + (u - gr * per) / 4, d = c / chunks, col = gr * 8 + g, m = s.tokens[d];
-            const bool in = kCompact ? int(col) < __popc(m) : (m >> col) & 1u;
-            const uint32_t row = s.off[d] + (kCompact ? col : uint32_t(__popc(m & ((1u << col) - 1u))));
+            const bool in = kCompact ? int(col) < left : (m >> col) & 1u;
+            const uint32_t row = s.off[d] + (kCompact ? first + col : uint32_t(__popc(m & ((1u << col) - 1u))));
             stage_unit(smem, u, in ? a.act + uint64_t(row) * I : nullptr, I, c - d * chunks, u % 4);
         }
         __syncthreads();
@@ -142,12 +152,15 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     const int col = k * 8 + 2 * q + (z & 1);
-                    if (col < __popc(m0)) s_mine[s.row_t[s.off[d0] + col] * 16 + g + (z >> 1) * 8] += acc[k][z];
+                    if (col < left) s_mine[s.row_t[s.off[d0] + first + col] * 16 + g + (z >> 1) * 8] += acc[k][z];
                     acc[k][z] = 0.0f;
                 }
             }
             __syncwarp();
         }
+        // the slice's next tokens, or the next slice
+        first = left > 8 * NG ? first + 8 * NG : 0u;
+        if (first == 0u) c0 += n;
     }
     if constexpr (!kCompact) store_group<NG>(s_mine, acc, 0);
     __syncthreads();
@@ -196,9 +209,7 @@ cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
 
 template <int F>
 cudaError_t launch_layer_fp4(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.T <= 8) return launch_ng<F, 1>(a, num_sms, stream);
-    if (a.T <= 16) return launch_ng<F, 2>(a, num_sms, stream);
-    return launch_ng<F, 4>(a, num_sms, stream);
+    return a.T <= 8 ? launch_ng<F, 1>(a, num_sms, stream) : launch_ng<F, 2>(a, num_sms, stream);
 }
 
 }  // namespace

@@ -103,22 +103,6 @@ inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bloc
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Blocks per cluster that split k for `tiles` row tiles on a device that holds
-// `slots` blocks at once, at most `most` (more would leave warps without work):
-// the smallest C with the fullest waves. A grid of 1.5 waves takes 2: the fc2
-// of a layer with 448 row tiles on 304 slots ran 974 us unsplit and 553 us
-// when 456 slots held it.
-inline uint32_t split_k(uint32_t tiles, uint32_t slots, uint32_t most) {
-    uint32_t best = 1;
-    double full = 0.0;
-    for (uint32_t c = 1; c <= 8 && (c == 1 || c <= most); ++c) {
-        const uint64_t n = uint64_t(tiles) * c, waves = (n + slots - 1) / slots;
-        const double f = double(n) / double(waves * slots);
-        if (f > full + 0.02) { full = f; best = c; }
-    }
-    return best;
-}
-
 // Dynamic shared memory beyond 48 KB has to be granted to a kernel once per
 // device; one object per kernel instantiation remembers where it was.
 struct SmemGrant {
@@ -137,6 +121,49 @@ struct SmemGrant {
             err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - int(at.sharedSizeBytes));
         if (err == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
         return err;
+    }
+};
+
+// Clusters of C blocks (C = 1 .. 8) of a kernel that one device holds at once,
+// asked once per device: with one large block per SM and the SMs of a graphics
+// cluster in odd numbers, far fewer than SMs / C (a GEMV in clusters of 7 ran
+// in three waves).
+struct ClusterSlots {
+    std::atomic<uint64_t> known[64][2] = {};   // per device: 16-bit counts of C = 1..4 and 5..8
+
+    template <typename Kernel>
+    cudaError_t get(Kernel kernel, uint32_t threads, size_t smem, int blocks, uint32_t (&slots)[9]) {
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        uint64_t v[2] = {0, 0};
+        if (dev < 64)
+            for (int i = 0; i < 2; ++i) v[i] = known[dev][i].load(std::memory_order_relaxed);
+        if (v[0] == 0 || v[1] == 0) {
+            v[0] = v[1] = 0;
+            for (uint32_t c = 1; c <= 8; ++c) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(c * 8);
+                cfg.blockDim = dim3(threads);
+                cfg.dynamicSmemBytes = smem;
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = c;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int n = blocks;   // a device's worth of single blocks
+                if (c > 1) {
+                    err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+                    if (err != cudaSuccess) return err;
+                }
+                v[(c - 1) / 4] |= uint64_t(std::max(1, std::min(n, 65535))) << (16 * ((c - 1) % 4));
+            }
+            if (dev < 64)
+                for (int i = 0; i < 2; ++i) known[dev][i].store(v[i], std::memory_order_relaxed);
+        }
+        for (uint32_t c = 1; c <= 8; ++c) slots[c] = uint32_t(v[(c - 1) / 4] >> (16 * ((c - 1) % 4))) & 65535u;
+        return cudaSuccess;
     }
 };
 
