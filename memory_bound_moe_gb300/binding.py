@@ -526,7 +526,7 @@ def _device(x: torch.Tensor) -> int:
     d = x.get_device()
     if d < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if d != torch.cuda.current_device():
+    if d != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
     return d
 
@@ -546,14 +546,17 @@ def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
     return 0 if t is None else _addr(t, name, dtype, shape, dev)
 
 
-def _new(shape: tuple, dtype: torch.dtype, x: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """Memory on x's device for a result. It comes from the current stream's
-    pool: when the work runs on another one it must not be handed out again
-    before that work is done."""
-    t = torch.empty(shape, dtype=dtype, device=x.device)
+def _kept(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A result's new memory comes from the current stream's pool: when the
+    work runs on another one it must not be handed out again before that work
+    is done."""
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _new(shape: tuple, dtype: torch.dtype, x: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    return _kept(torch.empty(shape, dtype=dtype, device=x.device), stream)
 
 
 def _raw_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
@@ -595,9 +598,11 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: t
     wp = _addr(weight, "weight", _bf16, (H,), dev)
     residual_out, rp, rop = _norm_residual(residual, residual_out, T, H, dev)
     if out is None:
-        out = _new((T, H), _bf16, x, stream)
-    st = _lib_fast().moe_add_rmsnorm(xp, rp, T, H, wp, weight_bias, eps, _addr(out, "out", _bf16, (T, H), dev), rop,
-                                     _raw_stream(stream, dev))
+        out = _kept(torch.empty_like(x), stream)
+        op = out.data_ptr()
+    else:
+        op = _addr(out, "out", _bf16, (T, H), dev)
+    st = _lib_fast().moe_add_rmsnorm(xp, rp, T, H, wp, weight_bias, eps, op, rop, _raw_stream(stream, dev))
     if st:
         raise MoeError("moe_add_rmsnorm", st)
     return out, residual_out
@@ -619,11 +624,16 @@ def moe_add_rmsnorm_mxfp8(x: torch.Tensor, residual: Optional[torch.Tensor], wei
     wp = _addr(weight, "weight", _bf16, (H,), dev)
     residual_out, rp, rop = _norm_residual(residual, residual_out, T, H, dev)
     if codes is None:
-        codes = _new((T, H), _u8, x, stream)
+        codes = _kept(torch.empty_like(x, dtype=_u8), stream)
+        cp = codes.data_ptr()
+    else:
+        cp = _addr(codes, "codes", _u8, (T, H), dev)
     if scales is None:
         scales = _new((T, H // 32), _u8, x, stream)
-    st = _lib_fast().moe_add_rmsnorm_mxfp8(xp, rp, T, H, wp, weight_bias, eps, _addr(codes, "codes", _u8, (T, H), dev),
-                                           _addr(scales, "scales", _u8, (T, H // 32), dev),
+        sp = scales.data_ptr()
+    else:
+        sp = _addr(scales, "scales", _u8, (T, H // 32), dev)
+    st = _lib_fast().moe_add_rmsnorm_mxfp8(xp, rp, T, H, wp, weight_bias, eps, cp, sp,
                                            _opt(out, "out", _bf16, (T, H), dev), rop, _raw_stream(stream, dev))
     if st:
         raise MoeError("moe_add_rmsnorm_mxfp8", st)
@@ -654,10 +664,12 @@ def moe_gemv_fp4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt
         raise TypeError(f"out: dtype {out_dtype}, expected torch.bfloat16 or torch.float32")
     if out is None:
         out = _new((T, N), out_dtype, x, stream)
+        op = out.data_ptr()
+    else:
+        op = _addr(out, "out", out_dtype, (T, N), dev)
     st = _lib_fast().moe_gemv_fp4(_addr(x, "x", _bf16, (T, K), dev), T, K, _addr(codes, "codes", _u8, (N, K // 2), dev),
-                                  _addr(scales, "scales", _u8, (N, K // block), dev), N, code, global_scale,
-                                  _addr(out, "out", out_dtype, (T, N), dev), out_dtype is _f32,
-                                  _raw_stream(stream, dev))
+                                  _addr(scales, "scales", _u8, (N, K // block), dev), N, code, global_scale, op,
+                                  out_dtype is _f32, _raw_stream(stream, dev))
     if st:
         raise MoeError("moe_gemv_fp4", st)
     return out

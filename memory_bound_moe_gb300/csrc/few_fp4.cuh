@@ -51,7 +51,7 @@ constexpr uint32_t kChunkK = 512;   // k per chunk
 #define MOE_FP4_WNV 20
 #endif
 #ifndef MOE_FP4_WMX
-#define MOE_FP4_WMX 16
+#define MOE_FP4_WMX 20
 #endif
 // Blocks are one per SM, of up to kMaxWarps warps (what the registers allow),
 // in RG row groups x KS splits of k.
@@ -123,23 +123,41 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
-// One unit of x: step i of chunk `chunk` of 8 rows (row: the lane group's, NULL
-// gives zeros), by one warp, to unit `to` of shared memory: for j = 0..3 the 16
-// bytes that every lane reads for word j of its granule.
-__device__ __forceinline__ void stage_unit(uint8_t* smem, uint32_t to, const uint16_t* row, uint32_t K, uint32_t chunk, uint32_t i) {
+// Units of x into shared memory, by all warps of the block: unit u is step u %
+// 4 of 8 rows; where(u, chunk) gives the lane group's row (NULL gives zeros)
+// and the chunk of k. For j = 0..3 a unit holds the 16 bytes that every lane
+// reads for word j of its granule. Two units' loads are in flight per warp.
+template <typename Where>
+__device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint32_t K, Where&& where) {
     const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
-    const uint32_t k0 = chunk * kChunkK + q * 128u + i * 32u;
-    uint4 x[4] = {};
-    if (row != nullptr && k0 < K) {
+    const uint32_t W = blockDim.x / kWarp;
+#pragma unroll 1
+    for (uint32_t u0 = threadIdx.x / kWarp; u0 < units; u0 += 2 * W) {
+        uint4 x[2][4] = {};
 #pragma unroll
-        for (int z = 0; z < 4; ++z) x[z] = __ldg(reinterpret_cast<const uint4*>(row + k0) + z);
+        for (uint32_t k = 0; k < 2; ++k) {
+            const uint32_t u = u0 + k * W;
+            if (u >= units) break;
+            uint32_t chunk;
+            const uint16_t* row = where(u, chunk);
+            const uint32_t k0 = chunk * kChunkK + q * 128u + u % 4 * 32u;
+            if (row != nullptr && k0 < K) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) x[k][z] = __ldg(reinterpret_cast<const uint4*>(row + k0) + z);
+            }
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) {
+            const uint32_t u = u0 + k * W;
+            if (u >= units) break;
+            uint32_t h[kXPairs];
+            const float inv = x_to_f16(x[k], h);
+            uint4* p = reinterpret_cast<uint4*>(smem + u * kUnit) + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j * 32] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+            if (q == 0) reinterpret_cast<float*>(smem + kInvAt)[u * 8 + g] = inv;
+        }
     }
-    uint32_t h[kXPairs];
-    const float inv = x_to_f16(x, h);
-    uint4* p = reinterpret_cast<uint4*>(smem + to * kUnit) + lane;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p[j * 32] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-    if (q == 0) reinterpret_cast<float*>(smem + kInvAt)[to * 8 + g] = inv;
 }
 
 // One lane's weights of a chunk: 64 bytes of its rows g and g + 8 of a tile,

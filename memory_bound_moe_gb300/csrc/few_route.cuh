@@ -23,6 +23,37 @@ struct FewRoute {
     int nd;                       // chosen experts
 };
 
+// What fc2 needs of it, left by fc1 in the workspace.
+struct FewRouteCopy {
+    uint32_t tokens[kMaxSlots];
+    uint16_t expert[kMaxSlots];
+    uint16_t off[kMaxSlots];
+    uint8_t row_t[kMaxSlots];
+    int nd;
+};
+static_assert(sizeof(FewRouteCopy) <= kFewRouteBytes, "workspace");
+
+__device__ __forceinline__ void save_route(FewRouteCopy* to, const FewRoute& s, int S) {
+    for (int i = threadIdx.x; i < S; i += int(blockDim.x)) {   // entries from nd on are not used
+        to->tokens[i] = s.tokens[i];
+        to->expert[i] = s.expert[i];
+        to->off[i] = s.off[i];
+        to->row_t[i] = s.row_t[i];
+    }
+    if (threadIdx.x == 0) to->nd = s.nd;
+}
+
+__device__ __forceinline__ void load_route(FewRoute& s, const FewRouteCopy* from, int S) {
+    for (int i = threadIdx.x; i < S; i += int(blockDim.x)) {
+        s.tokens[i] = from->tokens[i];
+        s.expert[i] = from->expert[i];
+        s.off[i] = from->off[i];
+        s.row_t[i] = from->row_t[i];
+    }
+    if (threadIdx.x == 0) s.nd = from->nd;
+    __syncthreads();
+}
+
 template <int EPL>
 __device__ __noinline__ int route_token(const RouteArgs& a, int t) {
     const int lane = threadIdx.x % kWarp;

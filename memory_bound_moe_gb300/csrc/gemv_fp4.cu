@@ -46,10 +46,11 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) gemv_kernel(G
     for (uint32_t s0 = c0; s0 < c1; s0 += slice) {
         const uint32_t n = min(slice, c1 - s0), per = n * 4;
         if (s0 > c0) __syncthreads();
-        for (uint32_t u = warp; u < per * groups; u += W) {
+        stage_units(smem, per * groups, a.K, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
             const uint32_t gr = u / per, r = gr * 8 + g;
-            stage_unit(smem, u, r < a.T ? a.x + uint64_t(r) * a.K : nullptr, a.K, s0 + (u - gr * per) / 4, u % 4);
-        }
+            chunk = s0 + (u - gr * per) / 4;
+            return r < a.T ? a.x + uint64_t(r) * a.K : nullptr;
+        });
         __syncthreads();
         const uint32_t k0 = n * ks / KS, k1 = n * (ks + 1) / KS;
         fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups, 1.0f);

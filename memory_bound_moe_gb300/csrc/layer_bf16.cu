@@ -10,8 +10,9 @@
 // its one rounding (tensor cores take bfloat16 operands), so the combine is a
 // plain sum over the concatenated k of all chosen experts, in float32.
 //
-// Routing is redundant: every block routes the whole batch in shared memory
-// (tens of KB of logits at most), so no block waits for another. A warp takes
+// Routing is redundant in fc1: every block routes the whole batch in shared
+// memory (tens of KB of logits at most), so no block waits for another; one
+// leaves it to fc2 in the workspace. A warp takes
 // tiles of 16 weight rows (few_device.cuh); the KS splits of k of a block sum
 // in shared memory.
 //   fc1: a tile is 8 gate rows and the same 8 up rows, so 8 columns of one
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kNt, NG == 4 ? 2 : 3) fc1_kernel(LayerArgs a, 
     __shared__ float s_part[kNw * 128];          // [warp][8 tokens][16 rows]
     pdl_wait_and_release();
     route_few(a, s, blockIdx.x == 0);
+    if (blockIdx.x == 0) save_route(static_cast<FewRouteCopy*>(a.route), s, a.T * a.k);
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, q = lane % 4;
     const int RG = kNw / KS, rg = warp / KS, ks = warp % KS;
     const uint32_t H = uint32_t(a.H), I = uint32_t(a.I), tiles = I / 8, chunks = (H + kChunk - 1) / kChunk;
@@ -144,11 +146,8 @@ __global__ void __launch_bounds__(kNt, NG == 4 ? 2 : 3) fc2_kernel(LayerArgs a, 
     const int RG = kNw / KS, rg = warp / KS, ks = warp % KS, rows = RG * 16;
     const uint32_t H = uint32_t(a.H), I = uint32_t(a.I), chunks = (I + kChunk - 1) / kChunk;
     const uint32_t rank = blockIdx.x % C, row0 = blockIdx.x / C * rows, mine = row0 + rg * 16 + g;
-    // Before the wait for fc1: routing from the logits. They are not written by
-    // fc1, and fc1 let this kernel start only after its own wait, so whatever
-    // wrote them has completed.
-    route_few(a, s, false);
     pdl_wait_and_release();
+    load_route(s, static_cast<const FewRouteCopy*>(a.route), a.T * a.k);
     const bool wide = rows_wide(I, a.w2);
     const uint32_t rows_ok = uint32_t(mine < H) | uint32_t(mine + 8 < H) << 1;
     // this warp's part of the (expert, chunk) list

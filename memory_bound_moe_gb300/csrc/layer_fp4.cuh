@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
     __shared__ FewRoute s;
     pdl_wait_and_release();
     route_few(a, s, blockIdx.x == 0);
+    if (blockIdx.x == 0) save_route(static_cast<FewRouteCopy*>(a.route), s, a.T * a.k);
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, q = lane % 4, W = blockDim.x / kWarp;
     const int RG = W / KS, rg = warp / KS, ks = warp % KS;
     const uint32_t H = uint32_t(a.H), I = uint32_t(a.I), tiles = I / 8, chunks = (H + kChunkK - 1) / kChunkK;
@@ -56,16 +57,12 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
             const uint32_t n = min(slice, chunks - s0), per = n * 4;
             if (staged != (x * 4u + first / 8u) * 4096u + s0) {   // s0 < 2048
                 __syncthreads();
-                for (uint32_t u = warp; u < per * groups; u += W) {
+                stage_units(smem, per * groups, H, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
                     const uint32_t gr = u / per, c = gr * 8 + g;
-                    const uint16_t* xr = nullptr;
-                    if (kCompact) {
-                        if (int(c) < left) xr = a.x + uint64_t(s.row_t[s.off[x] + first + c]) * H;
-                    } else if (int(c) < a.T) {
-                        xr = a.x + uint64_t(c) * H;
-                    }
-                    stage_unit(smem, u, xr, H, s0 + (u - gr * per) / 4, u % 4);
-                }
+                    chunk = s0 + (u - gr * per) / 4;
+                    if (kCompact) return int(c) < left ? a.x + uint64_t(s.row_t[s.off[x] + first + c]) * H : nullptr;
+                    return int(c) < a.T ? a.x + uint64_t(c) * H : nullptr;
+                });
                 __syncthreads();
                 staged = (x * 4u + first / 8u) * 4096u + s0;
             }
@@ -110,11 +107,8 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
     float* s_mine = s_part + warp * part;
     if (kCompact)
         for (int o = lane; o < part; o += kWarp) s_mine[o] = 0.0f;
-    // Before the wait for fc1: routing from the logits. They are not written by
-    // fc1, and fc1 let this kernel start only after its own wait, so whatever
-    // wrote them has completed.
-    route_few(a, s, false);
     pdl_wait_and_release();
+    load_route(s, static_cast<const FewRouteCopy*>(a.route), a.T * a.k);
     const Shape4 sh = fp4_shape<F>(8, I, a.w2);
     const uint32_t rows_ok = uint32_t(mine < H) | uint32_t(mine + 8 < H) << 1;
     const uint64_t all = uint64_t(s.nd) * chunks;
@@ -128,12 +122,12 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
         n = min(kUnits / 4 / groups, (kCompact ? min(c1, (d0 + 1) * chunks) : c1) - c0);
         const uint32_t per = n * 4;
         __syncthreads();
-        for (uint32_t u = warp; u < per * groups; u += W) {
+        stage_units(smem, per * groups, I, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
             const uint32_t gr = u / per, c = c0 + (u - gr * per) / 4, d = c / chunks, col = gr * 8 + g, m = s.tokens[d];
-            const bool in = kCompact ? int(col) < left : (m >> col) & 1u;
-            const uint32_t row = s.off[d] + (kCompact ? first + col : uint32_t(__popc(m & ((1u << col) - 1u))));
-            stage_unit(smem, u, in ? a.act + uint64_t(row) * I : nullptr, I, c - d * chunks, u % 4);
-        }
+            chunk = c - d * chunks;
+            if (kCompact ? int(col) >= left : !((m >> col) & 1u)) return nullptr;
+            return a.act + uint64_t(s.off[d] + (kCompact ? first + col : uint32_t(__popc(m & ((1u << col) - 1u))))) * I;
+        });
         __syncthreads();
         // this warp's share, expert by expert
         const uint32_t k1 = c0 + n * (ks + 1) / KS;

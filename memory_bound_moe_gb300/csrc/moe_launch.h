@@ -95,6 +95,7 @@ cudaError_t launch_gemv_fp4(const uint16_t* x, int T, int K, const uint8_t* code
 // A whole MoE layer for T <= 32 tokens (layer_kernels.cuh, one
 // translation unit per weight format). Weights: bfloat16 (w13,
 // w2), or codes with scales and, for NVFP4, a tensor scale per expert.
+constexpr size_t kFewRouteBytes = 4624;
 struct LayerArgs {
     const float* logits;
     const uint16_t* x;
@@ -108,6 +109,7 @@ struct LayerArgs {
     int32_t* topk_ids;           // may be NULL
     float* topk_weights;         // may be NULL
     uint16_t* act;               // workspace [T*k, I]
+    void* route;                 // workspace, kFewRouteBytes
     int T, E, k, renorm, H, I;
 };
 cudaError_t launch_layer_bf16(const LayerArgs& a, int num_sms, cudaStream_t stream);
