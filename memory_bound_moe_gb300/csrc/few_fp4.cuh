@@ -23,7 +23,9 @@
 //    each of its two rows, a "chunk" of 512 k per warp, in two 256-bit loads,
 //    their scales in one. A chunk is four steps of 128 k, granule i of every
 //    lane making step i. The next chunk's loads go out as soon as half of the
-//    registers is used up; 24 warps of 80 registers on an SM hide the rest.
+//    registers is used up; the other warps of the SM hide the rest.
+//  - MXFP4 chunks whose blocks need turns are only noted, and added by a second
+//    look at the tile behind the loop: what they need stays out of its registers.
 //  - x is converted once per block, into shared memory, in the order the B
 //    fragments are read: all distances in the loop are constants. (With the
 //    same data in global memory behind run-time strides the loop took 24
@@ -39,7 +41,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
+#include <cmath>
 #include <cstdint>
 
 namespace moe {
@@ -47,14 +49,10 @@ namespace moe {
 constexpr int kXPairs = 16;         // f16 pairs of one lane's x in a step
 constexpr uint32_t kChunkK = 512;   // k per chunk
 
-#ifndef MOE_FP4_WNV
-#define MOE_FP4_WNV 20
-#endif
-#ifndef MOE_FP4_WMX
-#define MOE_FP4_WMX 20
-#endif
-// Blocks are one per SM, of up to kMaxWarps warps (what the registers allow),
-// in RG row groups x KS splits of k.
+// Blocks are one per SM, of up to kMaxWarps warps (what the registers allow: 96
+// each with 20 warps, 128 with 16), in RG row groups x KS splits of k. With one
+// group of tokens 20 warps are the better for NVFP4; for MXFP4 they spill: the
+// layer of T=8, E=32, k=4, H=I=2880 takes 135 us with 20 and 117 with 16.
 constexpr uint32_t kUnits = 88;                       // (group, step) units of x that shared memory holds
 constexpr uint32_t kUnit = 2048;                      // one unit: 8 tokens x 128 k, f16
 constexpr uint32_t kInvAt = kUnits * kUnit;           // the units' inverse powers of two, 8 each
@@ -62,7 +60,7 @@ constexpr uint32_t kPartAt = kInvAt + kUnits * 32u;   // partial sums: [warp][to
 
 template <int F, int NG>
 struct Fp4Block {
-    static constexpr int kMaxWarps = NG == 1 ? (F == kWNvfp4 ? MOE_FP4_WNV : MOE_FP4_WMX) : 16;
+    static constexpr int kMaxWarps = NG == 1 && F == kWNvfp4 ? 20 : 16;
     static constexpr int kMaxThreads = kMaxWarps * kWarp;
     // partial sums of up to 32 tokens (8 if NG == 1)
     static constexpr uint32_t kSmem = kPartAt + kMaxWarps * (NG == 1 ? 512u : 2048u);
@@ -235,40 +233,52 @@ __device__ __forceinline__ void load_scales(WChunk4<F>& a, const Place4& at, con
 // MXFP4 blocks further apart than one window, with a NaN scale, or so small
 // that the factors' product could leave float32: turn by turn, each with the
 // largest scale among the blocks not yet added. Adds one group's products of a
-// step (its B fragments at xb) to acc; w [2][4] codes, sc [2] scales.
-static __device__ __noinline__ void mxfp4_apart(float* acc, const uint32_t* w, const uint32_t* sc, uint32_t xb, float f0, float f1) {
-    uint32_t todo = 3u;
-    while (__any_sync(kFull, todo != 0u)) {
-        uint32_t top = 0;
-        for (int k = 0; k < 2; ++k)
-            if (((todo >> k) & 1u) && sc[k] != 255u) top = max(top, sc[k]);
-        top = __reduce_max_sync(kFull, top);
-        const float fx = mxfp4_unit(top);
-        uint32_t s[2], left = 0;
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t* v = w + k * 4;
-            const int d = int(sc[k]) - int(top) + 28;   // biased f16 exponent
-            s[k] = 0;
-            if ((todo >> k) & 1u) {
-                if (sc[k] == 255u) s[k] = 0x7e007e00u;     // NaN
-                else if (d >= 1) s[k] = uint32_t(d) * 0x04000400u;
-                else if (((v[0] | v[1] | v[2] | v[3]) & 0x77777777u) != 0u) left |= 1u << k;
+// chunk (its B fragments at xb, its inverse powers of two at inv) to acc.
+__device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxfp4>& a, uint32_t xb, const float* inv, float f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f0 = inv[i * 8] * f, f1 = inv[i * 8 + 1] * f;
+        uint32_t todo = 3u, sc[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sc[k] = (a.s[k][i / 2] >> (8 * (i % 2))) & 255u;
+#pragma unroll 1
+        while (__any_sync(kFull, todo != 0u)) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (((todo >> k) & 1u) && sc[k] != 255u) top = max(top, sc[k]);
+            top = __reduce_max_sync(kFull, top);
+            const float fx = mxfp4_unit(top);
+            uint32_t s[2], left = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t(&v)[8] = a.w[k][i / 2].w;
+                const uint32_t codes = v[i % 2 * 4] | v[i % 2 * 4 + 1] | v[i % 2 * 4 + 2] | v[i % 2 * 4 + 3];
+                const int d = int(sc[k]) - int(top) + 28;   // biased f16 exponent
+                s[k] = 0;
+                if ((todo >> k) & 1u) {
+                    if (sc[k] == 255u) s[k] = 0x7e007e00u;     // NaN
+                    else if (d >= 1) s[k] = uint32_t(d) * 0x04000400u;
+                    else if ((codes & 0x77777777u) != 0u) left |= 1u << k;
+                }
             }
+            float c[4] = {};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t p0[4], p1[4];
+                e2m1_to_f16(a.w[0][i / 2].w[i % 2 * 4 + j], s[0], p0);
+                e2m1_to_f16(a.w[1][i / 2].w[i % 2 * 4 + j], s[1], p1);
+                const uint4 b = lds128(xb + i * kUnit + j * 512u);
+                mma_f16(c, p0[0], p1[0], p0[1], p1[1], b.x, b.y);
+                mma_f16(c, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
+            }
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const float fz = z & 1 ? f1 : f0;   // the smaller of the factors last: neither product leaves the range
+                acc[z] += fz <= 1.0f ? (c[z] * fz) * fx : (c[z] * fx) * fz;
+            }
+            todo = left;
         }
-        float c[4] = {};
-        for (int j = 0; j < 4; ++j) {
-            uint32_t p0[4], p1[4];
-            e2m1_to_f16(w[j], s[0], p0);
-            e2m1_to_f16(w[4 + j], s[1], p1);
-            const uint4 b = lds128(xb + j * 512u);
-            mma_f16(c, p0[0], p1[0], p0[1], p1[1], b.x, b.y);
-            mma_f16(c, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
-        }
-        for (int z = 0; z < 4; ++z) {
-            const float f = z & 1 ? f1 : f0;   // the smaller of the factors last: neither product leaves the range
-            acc[z] += f <= 1.0f ? (c[z] * f) * fx : (c[z] * fx) * f;
-        }
-        todo = left;
     }
 }
 
@@ -305,14 +315,45 @@ __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, 
     return top;
 }
 
+// Adds the chunks c0 .. c1 - 1 of a tile that need turns, and only those, to one
+// group's sums; x of chunk c0 begins at unit u0.
+__device__ __forceinline__ void mxfp4_apart_chunks(float* sums, const Place4* place, const Shape4* shape, uint32_t c0, uint32_t c1,
+                                                       uint8_t* smem, uint32_t u0, float f) {
+    const int lane = threadIdx.x % kWarp, q = lane % 4;
+    const Shape4 sh = *shape;
+    Place4 p = *place;
+    float acc[4] = {sums[0], sums[1], sums[2], sums[3]};
+    const uint32_t whole = __all_sync(kFull, p.rows == 3u) ? sh.whole : 0u;
+    p.w += c0 * 256u;
+    p.s += c0 * (kChunkK / WInfo<kWMxfp4>::kBlock);
+#pragma unroll 1
+    for (uint32_t c = c0; c < c1; ++c) {
+        WChunk4<kWMxfp4> a;
+        bool apart;
+        load_scales(a, p, sh, c, c < whole);
+        mxfp4_top(a, apart, p, sh, c, c < whole);
+        if (apart) {
+            const uint32_t n = row_granules(sh.rb, c), u = u0 + (c - c0) * 4;
+            load_rows(a.w, 0, p.w, sh.half_w, c < whole, p.rows, n, sh.whole > 0u);
+            load_rows(a.w, 1, p.w, sh.half_w, c < whole, p.rows, n, sh.whole > 0u);
+            mxfp4_apart(acc, a, uint32_t(__cvta_generic_to_shared(smem)) + u * kUnit + lane * 16u,
+                        reinterpret_cast<const float*>(smem + kInvAt) + u * 8 + 2 * q, f);
+        }
+        p.w += 256;
+        p.s += kChunkK / WInfo<kWMxfp4>::kBlock;
+    }
+#pragma unroll
+    for (int z = 0; z < 4; ++z) sums[z] = acc[z];
+}
+
 // The products of step i of a chunk with the first `groups` groups of 8 tokens.
 // xb[n]: this lane's B fragments of group n in the chunk's first unit, inv[n]:
 // that unit's inverse powers of two of the lane's two tokens in C, 2 q and 2 q
-// + 1; f multiplies the sums, top and apart as of mxfp4_top.
+// + 1; f multiplies the sums, top as of mxfp4_top.
 template <int F, int NG>
 __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& a, const uint32_t (&sc)[2][2],
                                          int i, const uint32_t (&xb)[NG], const float* (&inv)[NG], int groups, float f,
-                                         uint32_t top, bool apart) {
+                                         uint32_t top) {
     uint32_t s[2][2];   // f16 scale in both halves: [row g or g + 8][k 0..15 or 16..31 of the granule]
     if constexpr (F == kWNvfp4) {
 #pragma unroll
@@ -324,27 +365,6 @@ __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& 
             s[k][1] = __byte_perm(v, v, 0x3232);
         }
     } else {
-        if (apart) {
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                if (NG > 1 && n >= groups) break;
-                const float2 v = *reinterpret_cast<const float2*>(inv[n] + i * 8);
-                float t[4];
-                uint32_t w[2][4], x[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    x[h] = (sc[h][i / 2] >> (8 * (i % 2))) & 255u;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) w[h][z] = a.w[h][i / 2].w[(i % 2) * 4 + z];
-                }
-#pragma unroll
-                for (int z = 0; z < 4; ++z) t[z] = acc[n][z];
-                mxfp4_apart(t, &w[0][0], x, xb[n] + i * kUnit, v.x * f, v.y * f);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) acc[n][z] = t[z];
-            }
-            return;
-        }
         f *= mxfp4_unit(top);
         const uint32_t shift = (28u - top) * 0x04000400u;   // biased f16 exponent X - top + 28, in both halves
 #pragma unroll
@@ -379,7 +399,7 @@ __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& 
 // The chunks c0 .. c1 - 1 of one tile; x of chunk c0 begins at unit u0 of
 // shared memory, each group's `group_units` behind the one before.
 template <int F, int NG>
-__device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Shape4& sh, uint32_t c0, uint32_t c1,
+__device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], const Place4& p0, const Shape4& sh, uint32_t c0, uint32_t c1,
                                          uint8_t* smem, uint32_t u0, uint32_t group_units, int groups, float f) {
     if (c0 >= c1) return;
     const int lane = threadIdx.x % kWarp, q = lane % 4;
@@ -391,7 +411,9 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Sh
         xb[n] = uint32_t(__cvta_generic_to_shared(smem)) + u * kUnit + lane * 16u;
         inv[n] = reinterpret_cast<const float*>(smem + kInvAt) + u * 8 + 2 * q;
     }
-    const uint32_t whole = __all_sync(kFull, p.rows == 3u) ? sh.whole : 0u;   // chunks below it are whole
+    const uint32_t whole = __all_sync(kFull, p0.rows == 3u) ? sh.whole : 0u;   // chunks below it are whole
+    bool some = false;   // MXFP4: whether chunks were left out, whose blocks need turns
+    Place4 p = p0;
     p.w += c0 * 256u;
     p.s += c0 * (kChunkK / WInfo<F>::kBlock);
     WChunk4<F> a;
@@ -412,11 +434,16 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Sh
         p.w += 256;
         p.s += kChunkK / WInfo<F>::kBlock;
         if (more) load_scales(a, p, sh, c + 1, c + 1 < whole);
-        fp4_step<F, NG>(acc, a, sc, 0, xb, inv, groups, f, top, apart);
-        fp4_step<F, NG>(acc, a, sc, 1, xb, inv, groups, f, top, apart);
+        some |= apart;
+        if (!apart) {
+            fp4_step<F, NG>(acc, a, sc, 0, xb, inv, groups, f, top);
+            fp4_step<F, NG>(acc, a, sc, 1, xb, inv, groups, f, top);
+        }
         if (more) load_rows(a.w, 0, p.w, sh.half_w, c + 1 < whole, p.rows, row_granules(sh.rb, c + 1), sh.whole > 0u);
-        fp4_step<F, NG>(acc, a, sc, 2, xb, inv, groups, f, top, apart);
-        fp4_step<F, NG>(acc, a, sc, 3, xb, inv, groups, f, top, apart);
+        if (!apart) {
+            fp4_step<F, NG>(acc, a, sc, 2, xb, inv, groups, f, top);
+            fp4_step<F, NG>(acc, a, sc, 3, xb, inv, groups, f, top);
+        }
         if (more) load_rows(a.w, 1, p.w, sh.half_w, c + 1 < whole, p.rows, row_granules(sh.rb, c + 1), sh.whole > 0u);
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -424,19 +451,40 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], Place4 p, const Sh
             inv[n] += 32;
         }
     }
+    if constexpr (F == kWMxfp4) {
+        if (some) {   // rare: a second look at the tile, for the chunks left out
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                if (NG > 1 && n >= groups) break;
+                float v[4] = {acc[n][0], acc[n][1], acc[n][2], acc[n][3]};
+                const Place4 place = p0;
+                const Shape4 shape = sh;
+                mxfp4_apart_chunks(v, &place, &shape, c0, c1, smem, u0 + n * group_units, f);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) acc[n][z] = v[z];
+            }
+        }
+    }
 }
 
 // How a kernel of one block per SM over `tiles` row tiles divides its work: W
 // warps per block, KS splits of k in a block, C blocks of a cluster, that share
-// the `chunks` of a tile. The least of a simple estimate in microseconds: a
-// wave of blocks pays about 2.5 for launch and sums (1 more for a cluster),
-// 0.4 per unit of x a warp converts, and per chunk 0.25 for every warp of a
-// scheduler, but no less than a load's latency, 1.0.
+// the `chunks` of a tile, each for `groups` groups of 8 tokens (on average), of
+// `outs` that the results have. The least of an estimate in microseconds, its
+// constants fitted to 60 measured divisions of the workloads' shapes: a wave of
+// blocks pays 2 for launch and sums (1 more for a cluster) and 0.15 for every
+// tile and group it adds up, 0.6 per unit of x that a warp converts, 1.5 for
+// every further filling of shared memory, and per chunk 0.25 for every warp of
+// a scheduler and as much per group, but no less than a load's latency, 1.0.
+// The least is also what measured best, e.g. T=32, N=5760, K=2880: 15.4 us with
+// (16, 2, 3), 19.8 with (16, 1, 6); T=7, N=28672, K=4096: 19.2 with (12, 1, 1),
+// 20.8 with (16, 1, 1).
 struct Fp4Split {
     uint32_t w, ks, c;
 };
-inline Fp4Split fp4_split(uint64_t tiles, uint32_t chunks, uint32_t groups, uint32_t max_warps, const uint32_t (&slots)[9]) {
+inline Fp4Split fp4_split(uint64_t tiles, uint32_t chunks, double groups, uint32_t outs, uint32_t max_warps, const uint32_t (&slots)[9]) {
     Fp4Split best = {max_warps, 1, 1};
+    const uint32_t room = std::max(1u, kUnits / 4 / uint32_t(groups + 0.999));   // chunks of x in shared memory
     double least = 1e30;
     for (uint32_t w = 4; w <= max_warps; w += 4)
         for (uint32_t ks = 1; ks <= w && ks <= chunks; ++ks) {
@@ -444,10 +492,12 @@ inline Fp4Split fp4_split(uint64_t tiles, uint32_t chunks, uint32_t groups, uint
             for (uint32_t c = 1; c <= 8 && (c == 1 || c * ks <= chunks); ++c) {
                 const uint32_t rg = w / ks, share = (chunks + c - 1) / c;
                 const uint64_t waves = ((tiles + rg - 1) / rg + slots[c] - 1) / slots[c];
-                const double chunk = std::max(1.0, 0.25 * (w / 4.0) * (0.6 + 0.4 * groups));
-                const double convert = 0.4 * ((share * 4 * groups + w - 1) / w);
-                const double t = double(waves) * (2.5 + (c > 1 ? 1.0 : 0.0) + convert + chunk * ((share + ks - 1) / ks));
-                if (t < least * 0.98) {
+                const uint32_t fills = (share + room - 1) / room, per_fill = (share + fills - 1) / fills;
+                const double chunk = std::max(1.0, 0.125 * w * (0.5 + 0.5 * groups));
+                const double convert = 0.6 * std::ceil(share * 4 * groups / w);
+                const double t = double(waves) * (2.0 + (c > 1 ? 1.0 : 0.0) + 0.15 * outs * rg + convert + 1.5 * (fills - 1) +
+                                                  chunk * fills * ((per_fill + ks - 1) / ks));
+                if (t < least * 0.99) {
                     least = t;
                     best = {w, ks, c};
                 }

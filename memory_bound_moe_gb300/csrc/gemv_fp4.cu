@@ -86,7 +86,7 @@ cudaError_t launch_ng(GemvArgs a, int num_sms, cudaStream_t stream) {
     if (err == cudaSuccess) err = clusters.get(kernel, B::kMaxThreads, B::kSmem, num_sms, slots);
     if (err != cudaSuccess) return err;
     a.chunks = (a.K + kChunkK - 1) / kChunkK;
-    const Fp4Split sp = fp4_split((uint64_t(a.N) + 15) / 16, a.chunks, (a.T + 7) / 8, B::kMaxWarps, slots);
+    const Fp4Split sp = fp4_split((uint64_t(a.N) + 15) / 16, a.chunks, (a.T + 7) / 8, (a.T + 7) / 8, B::kMaxWarps, slots);
     const uint32_t rows = sp.w / sp.ks * 16, tiles = (a.N + rows - 1) / rows;
     return launch_cluster(kernel, dim3(tiles * sp.c), dim3(sp.w * kWarp), sp.c, B::kSmem, stream, a,
                           int(sp.ks), sp.c);

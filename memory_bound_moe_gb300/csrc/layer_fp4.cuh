@@ -195,7 +195,8 @@ cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
     const uint32_t grid = uint32_t(std::min<uint64_t>((most * ks + w - 1) / w, sms));
     err = launch_pdl(fc1, dim3(grid), dim3(w * kWarp), B::kSmem, stream, a, int(ks));
     if (err != cudaSuccess) return err;
-    const Fp4Split sp = fp4_split((uint64_t(a.H) + 15) / 16, uint32_t(nd * chunks2), 1, kMax, slots);
+    const Fp4Split sp = fp4_split((uint64_t(a.H) + 15) / 16, uint32_t(nd * chunks2), NG == 1 ? 1.0 : std::max(1.0, 0.4 + a.T * a.k / (8.0 * nd)),
+                                  (uint32_t(a.T) + 7) / 8, kMax, slots);
     const uint32_t rows = sp.w / sp.ks * 16, tiles = (uint32_t(a.H) + rows - 1) / rows;
     return launch_cluster(fc2, dim3(tiles * sp.c), dim3(sp.w * kWarp), sp.c, B::kSmem, stream, a,
                           int(sp.ks), sp.c);
