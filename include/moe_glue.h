@@ -422,7 +422,10 @@ moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residu
  * global_scale): codes [N, K/2], scales [N, K/32] (MXFP4) or [N, K/16]
  * (NVFP4), row-major. y [T, N], bfloat16 (rounded once) or, with y_float32
  * != 0, float32 (logits). The weights' values are exact; a scale byte that
- * encodes NaN makes its block NaN.
+ * encodes NaN makes its block NaN. x enters in f16 times a power of two per
+ * token and 128 k: exact down to 2^-32 of the largest of those 128 values;
+ * smaller ones lose at most 2^-39 of it. (The same for x and a in
+ * moe_layer_fp4.)
  * T <= MOE_FEW_MAX_TOKENS and K <= 2^20 (MOE_ERR_UNSUPPORTED); K a multiple
  * of 32, x, codes and scales 16-byte, y 4-byte aligned (MOE_ERR_MISALIGNED);
  * N any positive number. Results do not depend on timing; needs no workspace.

@@ -116,6 +116,8 @@ def _check(fn: str, status: int):
 def _stream_ptr(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
     if stream is not None:
         return stream.cuda_stream
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
     # the current stream's handle without building a Stream object (2 us a call)
     return torch._C._cuda_getCurrentRawStream(device.index)
 
@@ -546,21 +548,26 @@ def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
     return 0 if t is None else _addr(t, name, dtype, shape, dev)
 
 
-def _kept(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A result's new memory comes from the current stream's pool: when the
-    work runs on another one it must not be handed out again before that work
-    is done."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(shape: tuple, dtype: torch.dtype, x: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """New memory for the call. With a stream of its own it comes from that
+    stream's pool (another's might still be written by work that is pending
+    there), and is handed out again only after what the current stream has
+    done with it by then."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=x.device)
+    t.record_stream(current)
     return t
 
 
-def _new(shape: tuple, dtype: torch.dtype, x: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    return _kept(torch.empty(shape, dtype=dtype, device=x.device), stream)
-
-
 def _raw_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _lib_fast():
@@ -598,7 +605,7 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: t
     wp = _addr(weight, "weight", _bf16, (H,), dev)
     residual_out, rp, rop = _norm_residual(residual, residual_out, T, H, dev)
     if out is None:
-        out = _kept(torch.empty_like(x), stream)
+        out = torch.empty_like(x) if stream is None else _new((T, H), _bf16, x, stream)
         op = out.data_ptr()
     else:
         op = _addr(out, "out", _bf16, (T, H), dev)
@@ -624,7 +631,7 @@ def moe_add_rmsnorm_mxfp8(x: torch.Tensor, residual: Optional[torch.Tensor], wei
     wp = _addr(weight, "weight", _bf16, (H,), dev)
     residual_out, rp, rop = _norm_residual(residual, residual_out, T, H, dev)
     if codes is None:
-        codes = _kept(torch.empty_like(x, dtype=_u8), stream)
+        codes = _new((T, H), _u8, x, stream)
         cp = codes.data_ptr()
     else:
         cp = _addr(codes, "codes", _u8, (T, H), dev)

@@ -11,7 +11,7 @@
 //    its inverse. A value 2^-32 of the step's largest still keeps its 8 bits;
 //    what smaller ones lose is under 2^-39 of the largest.
 //  - MXFP4: an E8M0 scale enters as 2^(X - Xmax + 13), Xmax the largest of the
-//    warp's blocks in the step, and 2^(Xmax - 13) multiplies the sums. Where
+//    warp's blocks in a chunk of 512 k, and 2^(Xmax - 13) multiplies the sums. Where
 //    blocks lie more than 2^27 apart they take turns, each with its own Xmax.
 //  - NVFP4: E4M3 scales and their products with E2M1 are within f16's range.
 //

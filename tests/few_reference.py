@@ -2,8 +2,9 @@
 
 Bounds. A float32 sum of n terms loses at most about n * 2^-23 of the sum of
 their magnitudes (tensor-core additions may truncate: 2^-23, not 2^-24, each).
-A warp adds the products of 16 k at a time and the k are split over at least 8
-warps, whose sums are added last: n <= K/64 + 64 covers every split. Rounding
+A warp adds the products of 16 k at a time, which is 16 additions inside and one
+to the running sum; up to 20 splits of k in a block and 8 blocks are added last,
+and the widths' tails: n <= K/16 + 16 + 28 + 20. Rounding
 to bfloat16 is off by at most half a step, 2^-8 of the value, and by 2^-134 at
 the bottom of the range."""
 from __future__ import annotations
@@ -16,7 +17,7 @@ HALF = 2.0 ** -8
 
 
 def fsum(K):
-    return (K / 64 + 64) * 2.0 ** -23
+    return (K / 16 + 64) * 2.0 ** -23
 
 
 def e2m1(codes):

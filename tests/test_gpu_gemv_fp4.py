@@ -143,3 +143,31 @@ def test_outputs_behind_the_batch_stay_and_graph_replays(dev):
     s.synchronize()
     assert torch.equal(y, y2)
     assert moe_gemv_fp4(x[:0], cd, sd, "nvfp4").shape == (0, N)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,N,K", [(2, 17, 1 << 20), (9, 3, (1 << 20) - 32), (32, 70001, 32)])
+def test_largest_widths(dev, T, N, K, fmt):
+    from memory_bound_moe_gb300 import moe_gemv_fp4
+    x, codes, scales, cd, sd = make(T, N, K, fmt, dev, 12)
+    y = moe_gemv_fp4(x, cd, sd, fmt, 1.0, out_dtype=torch.float32)
+    check_gemv(y, x, weights64(codes, scales, fmt), f"T={T} N={N} K={K}")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [4, 12, 32])
+def test_operands_at_16_bytes(dev, fmt, T):
+    """Every operand 16, but not 32 bytes behind a boundary: the same bits."""
+    from memory_bound_moe_gb300 import moe_gemv_fp4
+
+    def moved(t):
+        b = t.contiguous().view(torch.uint8).flatten()
+        buf = torch.empty(b.numel() + 64, dtype=torch.uint8, device=dev)
+        assert buf.data_ptr() % 32 == 0
+        return buf[16:16 + b.numel()].copy_(b).view(t.dtype).view(t.shape)
+
+    for N, K in ((40, 1024), (33, 2880)):
+        x, codes, scales, cd, sd = make(T, N, K, fmt, dev, 13)
+        y = moe_gemv_fp4(x, cd, sd, fmt, 2.0)
+        check_gemv(y, x, weights64(codes, scales, fmt, 2.0 if fmt == "nvfp4" else 1.0), "aligned")
+        assert torch.equal(y, moe_gemv_fp4(moved(x), moved(cd), moved(sd), fmt, 2.0))

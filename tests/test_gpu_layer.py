@@ -196,6 +196,86 @@ def test_buffers_streams_and_graphs(dev, fmt):
         assert all(torch.equal(r, g) for g in gs)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_operands_at_16_bytes(dev, fmt):
+    """x and the weights 16, but not 32 bytes behind a boundary: the same bits."""
+    def moved(t):
+        b = t.contiguous().view(torch.uint8).flatten()
+        buf = torch.empty(b.numel() + 64, dtype=torch.uint8, device=dev)
+        assert buf.data_ptr() % 32 == 0
+        return buf[16:16 + b.numel()].copy_(b).view(t.dtype).view(t.shape)
+
+    for T in (3, 20):
+        layer = Layer(6, 608, 320, fmt, dev, 14)
+        logits, x = tokens(T, 6, 608, dev, 15)
+        want = run_and_check(layer, logits, x, 2, True, "aligned")
+        if fmt == "bf16":
+            layer.w13, layer.w2 = moved(layer.w13), moved(layer.w2)
+        else:
+            layer.d = [moved(t) for t in layer.d]
+        assert torch.equal(want, layer(logits, moved(x), 2, True))
+
+
+@pytest.mark.parametrize("T,H,I,fmt", [(1, 8, 1 << 20, "bf16"), (2, 1 << 20, 8, "bf16"), (1, 32, (1 << 20) - 32, "nvfp4"),
+                                       (9, 1 << 20, 32, "mxfp4"), (3, 1 << 20, 32, "nvfp4")])
+def test_largest_widths(dev, T, H, I, fmt):
+    layer = Layer(1, H, I, fmt, dev, 16)
+    logits, x = tokens(T, 1, H, dev, 17)
+    run_and_check(layer, logits, x, 1, False, f"T={T} H={H} I={I} {fmt}")
+
+
+def test_new_memory_with_a_stream_of_its_own(dev):
+    """Results and workspace of a call on another stream: not memory that the
+    current stream still writes."""
+    layer = Layer(8, 256, 128, "bf16", dev, 18)
+    logits, x = tokens(4, 8, 256, dev, 19)
+    want = layer(logits, x, 2, True)
+    s = torch.cuda.Stream()
+    slow = torch.randn(4096, 4096, device=dev)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        slow = (slow @ slow).clamp_(-1, 1)                             # the current stream is busy
+        freed = [torch.empty_like(want).fill_(9) for _ in range(4)]   # written when its turn comes
+        del freed
+        got = layer(logits, x, 2, True, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+FIRST = """
+import torch
+from memory_bound_moe_gb300 import moe_add_rmsnorm, moe_gemv_fp4, moe_layer, moe_layer_fp4
+dev = torch.device("cuda:0")
+T, E, H, I = 4, 8, 128, 64
+bf = lambda *s: torch.randn(*s, device=dev).to(torch.bfloat16)
+u8 = lambda *s: torch.randint(1, 100, s, device=dev, dtype=torch.uint8)
+x, logits, w13, w2 = bf(T, H), torch.randn(T, E, device=dev), bf(E, 2 * I, H), bf(E, H, I)
+q = (u8(E, 2 * I, H // 2), u8(E, 2 * I, H // 16), u8(E, H, I // 2), u8(E, H, I // 16))
+g = torch.ones(E, device=dev)
+def step():
+    return (moe_add_rmsnorm(x, None, w2[0, :, 0].contiguous())[0], moe_gemv_fp4(x, q[0][0], q[1][0]),
+            moe_layer(logits, x, w13, w2, 2, True), moe_layer_fp4(logits, x, *q, 2, True, "nvfp4", g, g))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+eager = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture(dev):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
 def test_back_to_back_calls_that_feed_each_other(dev):
     """Every call reads the previous one's output (x and, through a product,
     the logits): launches that overlap must not read early."""
