@@ -3,10 +3,15 @@
 // W in the library's MXFP4 or NVFP4 layout (codes [N, K/2], scales
 // [N, K/block]). Bound by the weights' bytes (0.53 or 0.56 per value).
 //
-// A block takes 16 rows per row group; its row groups share x, its
-// KS splits and the C blocks of its cluster share k (few_fp4.cuh). The partial sums meet
+// A block takes 16 rows per row group; its row groups share x, its KS splits
+// and the C blocks of its cluster share k (few_fp4.cuh). The partial sums meet
 // in shared memory, then through distributed shared memory, always in the same
 // order: results do not depend on timing.
+//
+// Measured on GB300 in graphs: T=7, N=28672, K=4096 NVFP4 19.3 us (3.4 TB/s of
+// weights, half the copy rate, bound by the loop's instructions); T=16, N=4096,
+// K=7168 NVFP4 12.7 us, T=32, N=5760, K=2880 MXFP4 14.6 us, T=1, N=2048, K=768
+// MXFP4 4.1 us (latency: launch, x to f16, one or two chunks per warp, sums).
 #include "few_fp4.cuh"
 #include "moe_launch.h"
 #include "rows_common.cuh"

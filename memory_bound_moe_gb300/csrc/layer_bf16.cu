@@ -12,9 +12,8 @@
 //
 // Routing is redundant in fc1: every block routes the whole batch in shared
 // memory (tens of KB of logits at most), so no block waits for another; one
-// leaves it to fc2 in the workspace. A warp takes
-// tiles of 16 weight rows (few_device.cuh); the KS splits of k of a block sum
-// in shared memory.
+// leaves it to fc2 in the workspace. A warp takes tiles of 16 weight rows
+// (few_device.cuh); the KS splits of k of a block sum in shared memory.
 //   fc1: a tile is 8 gate rows and the same 8 up rows, so 8 columns of one
 //        expert's activation; a block takes an even share of all tiles. B
 //        columns are the expert's own tokens. The activation is stored
@@ -24,6 +23,10 @@
 //        columns are the tokens themselves, zero where a token is not routed to
 //        the expert, so the sums stay in registers to the end.
 // All sums are taken in a fixed order: results do not depend on timing.
+//
+// Measured on GB300 in graphs: T=16, E=256, k=8, H=7168, I=2048 1.25-1.29 ms
+// (fc1 829-862 us, fc2 427-446 us), the copy rate; T=1, E=128, k=8, H=2048,
+// I=768 26.6 us where the bytes take 11.3 (launches, routing, short rows).
 #include "few_device.cuh"
 #include "few_route.cuh"
 #include "moe_launch.h"
@@ -184,7 +187,7 @@ template <int NG>
 cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
     auto fc1 = fc1_kernel<NG>;
     auto fc2 = fc2_kernel<NG>;
-    constexpr uint32_t kPerSm = NG == 4 ? 2 : 3;
+    constexpr uint32_t kPerSm = NG == 4 ? 2 : 3;   // what the registers allow; T=16 with 2: 1.55 ms, with 3: 1.25
     static ClusterSlots clusters;
     const uint32_t slots1 = kPerSm * uint32_t(num_sms);
     uint32_t slots[9];
@@ -194,7 +197,8 @@ cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
     double miss = 1.0;
     for (int t = 0; t < a.T; ++t) miss *= 1.0 - double(a.k) / a.E;
     const double nd = std::max<double>(a.k, a.E * (1.0 - miss));
-    // fc1: splits of k until every warp has about three pieces (the last then costs little)
+    // fc1: splits of k until every warp has about three pieces (the last then costs little; one, three and six
+    // pieces are within 0.4%)
     const uint32_t chunks1 = (uint32_t(a.H) + kChunk - 1) / kChunk;
     const uint64_t tiles1 = uint64_t(nd * (a.I / 8)), most = std::min<uint64_t>(a.E, uint64_t(a.T) * a.k) * uint64_t(a.I / 8);
     uint32_t ks = 1;
@@ -202,7 +206,8 @@ cudaError_t launch_ng(const LayerArgs& a, int num_sms, cudaStream_t stream) {
     const uint32_t grid = uint32_t(std::min<uint64_t>((most * ks + kNw - 1) / kNw, slots1));
     err = launch_pdl(fc1, dim3(grid), dim3(kNt), 0, stream, a, int(ks));
     if (err != cudaSuccess) return err;
-    // fc2: of the splits (KS in a block, C blocks) the one with the fullest waves, then the fewest
+    // fc2: of the splits (KS in a block, C blocks) the one with the fullest waves, then the fewest (one token, H=2048,
+    // I=768: 26.4 us, 27.2 without clusters)
     const uint32_t chunks2 = uint32_t(nd * ((uint32_t(a.I) + kChunk - 1) / kChunk));
     uint32_t KS = 1, C = 1;
     double full = -1.0;

@@ -129,6 +129,46 @@ def test_equals_the_call_by_call_path(dev, fmt):
     assert rel <= 3 * 2.0 ** -8, rel
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 6, 19])
+def test_decode_step_in_a_graph(dev, fmt, T):
+    """Norm with the residual, 4-bit router and layer, as one captured step
+    that is replayed on new tokens: each call against its definition."""
+    from few_reference import check_gemv
+    from memory_bound_moe_gb300 import moe_add_rmsnorm, moe_gemv_fp4, moe_layer_workspace_size
+    E, k, H, I = 24, 4, 288, 160
+    layer = Layer(E, H, I, fmt, dev, 20)
+    rc, rs = random_fp4(np.random.default_rng(21), (E, H), fmt)
+    rg = 300.0 if fmt == "nvfp4" else 1.0
+    rcd, rsd = torch.from_numpy(rc).to(dev), torch.from_numpy(rs).to(dev)
+    weight = torch.ones(H, dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(moe_layer_workspace_size(T, E, k, H, I), dtype=torch.uint8, device=dev)
+    x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    residual = torch.zeros_like(x)
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    wts = torch.empty((T, k), dtype=torch.float32, device=dev)
+
+    def step():
+        y, _ = moe_add_rmsnorm(x, residual, weight)
+        logits = moe_gemv_fp4(y, rcd, rsd, fmt, rg, out_dtype=torch.float32)
+        return y, logits, layer(logits, y, k, True, topk_ids=ids, topk_weights=wts, workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, logits, out = step()
+    for rep in range(3):
+        x.copy_(torch.randn((T, H), generator=torch.Generator().manual_seed(rep)).to(torch.bfloat16))
+        sum_ = residual.double().cpu() + x.double().cpu()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(residual.cpu(), sum_.float().to(torch.bfloat16))
+        ref = sum_ / torch.sqrt((sum_ ** 2).mean(1, keepdim=True) + 1e-6)
+        # half a step of bfloat16, and the float32 sum, root and products: 2^-16
+        assert ((y.double().cpu() - ref).abs() <= (2.0 ** -8 + 2.0 ** -16) * ref.abs() + 2.0 ** -134).all()
+        check_gemv(logits, y, weights64(rc, rs, fmt, rg), "router")
+        check_layer(out, ids.cpu().numpy(), wts.double().cpu().numpy(), y, layer.values, H, I, "layer")
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_unchosen_weights_do_not_matter_and_tokens_stay_apart(dev, fmt):
     E, H, I, T, k = 12, 64, 64, 10, 2
