@@ -19,20 +19,6 @@
 
 namespace moe {
 
-enum WFmt { kWBf16 = 0, kWNvfp4 = 1, kWMxfp4 = 2 };
-
-template <int F>
-struct WInfo {
-    static constexpr bool kFp4 = F != kWBf16;
-    static constexpr int kBlock = F == kWNvfp4 ? 16 : 32;       // values per scale
-};
-
-// Bytes of a weight row of K values, and its scales.
-template <int F>
-__host__ __device__ constexpr uint32_t row_bytes(uint32_t K) { return WInfo<F>::kFp4 ? K / 2 : K * 2; }
-template <int F>
-__host__ __device__ constexpr uint32_t row_scales(uint32_t K) { return K / WInfo<F>::kBlock; }
-
 // 16-byte granules of a lane's 64 bytes of chunk c that lie in a row of rb bytes.
 __device__ __forceinline__ uint32_t row_granules(uint32_t rb, uint32_t c) {
     const uint32_t at = c * 256u + (threadIdx.x % 4) * 64u;

@@ -46,6 +46,17 @@
 
 namespace moe {
 
+enum WFmt { kWNvfp4 = 1, kWMxfp4 = 2 };
+
+template <int F>
+struct WInfo {
+    static constexpr int kBlock = F == kWNvfp4 ? 16 : 32;   // values per scale
+};
+
+// Scales of a weight row of K values.
+template <int F>
+__host__ __device__ constexpr uint32_t row_scales(uint32_t K) { return K / WInfo<F>::kBlock; }
+
 constexpr int kXPairs = 16;         // f16 pairs of one lane's x in a step
 constexpr uint32_t kChunkK = 512;   // k per chunk
 
@@ -183,7 +194,7 @@ struct Shape4 {
 
 template <int F>
 __device__ __forceinline__ Shape4 fp4_shape(uint64_t half_rows, uint32_t K, const void* w) {
-    const uint32_t rb = row_bytes<F>(K), rs = row_scales<F>(K);
+    const uint32_t rb = K / 2, rs = row_scales<F>(K);
     const uint32_t al = rs & (0u - rs);   // largest power of two that divides a row's scales
     const bool wide = rb % 32u == 0u && reinterpret_cast<uintptr_t>(w) % 32u == 0u;
     return {half_rows * rb, half_rows * rs, rb, wide ? rb / 256u : 0u, int(min(al, 8u))};

@@ -92,9 +92,9 @@ cudaError_t launch_gemv_fp4(const uint16_t* x, int T, int K, const uint8_t* code
                             int N, bool nvfp4, float g, void* y, bool y_f32, int num_sms,
                             cudaStream_t stream);
 
-// A whole MoE layer for T <= 32 tokens (layer_kernels.cuh, one
-// translation unit per weight format). Weights: bfloat16 (w13,
-// w2), or codes with scales and, for NVFP4, a tensor scale per expert.
+// A whole MoE layer for T <= 32 tokens (layer_bf16.cu, layer_fp4.cuh). Weights:
+// bfloat16 (w13, w2), or codes with scales and, for NVFP4, a tensor scale per
+// expert. kFewRouteBytes: the routing that fc1 leaves for fc2 (few_route.cuh).
 constexpr size_t kFewRouteBytes = 4624;
 struct LayerArgs {
     const float* logits;
