@@ -120,12 +120,13 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
     const uint64_t all = uint64_t(s.nd) * chunks;
     const uint32_t c1 = uint32_t(all * (rank + 1) / C);
     float acc[NG][4] = {};
-    uint32_t n, first = 0;   // first: the pass's first token of the expert
+    uint32_t n = 0, first = 0;   // first: the pass's first token of the expert
     for (uint32_t c0 = uint32_t(all * rank / C); c0 < c1;) {
-        // the slice: chunks c0 .. c0 + n - 1 of the list, for 8 NG tokens of the expert if kCompact
+        // the slice: chunks c0 .. c0 + n - 1 of the list, for 8 NG tokens of the expert if kCompact; its first pass,
+        // which has the most groups, says how long it is, and every pass covers the same chunks
         const uint32_t d0 = c0 / chunks;
         const int left = kCompact ? __popc(s.tokens[d0]) - int(first) : 8, groups = min(NG, (left + 7) / 8);
-        n = min(kUnits / 4 / groups, (kCompact ? min(c1, (d0 + 1) * chunks) : c1) - c0);
+        if (first == 0u) n = min(kUnits / 4 / groups, (kCompact ? min(c1, (d0 + 1) * chunks) : c1) - c0);
         const uint32_t per = n * 4;
         __syncthreads();
         stage_units(smem, per * groups, I, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
