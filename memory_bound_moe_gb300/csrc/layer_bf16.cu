@@ -168,7 +168,17 @@ __global__ void __launch_bounds__(kNt, NG == 4 ? 2 : 3) fc2_kernel(LayerArgs a, 
             live |= uint32_t(((m >> (8 * n)) & 0xffu) != 0u) << n;
         }
         const Rows p = {static_cast<const uint8_t*>(a.w2) + (uint64_t(s.expert[d]) * H + mine) * (2 * I) + q * 64, 8ull * (2 * I), rows_ok};
+        float before[NG][4];
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) before[n][z] = acc[n][z];
         bf16_tile<NG>(acc, p, I, wide, k0, k1, x, live);
+        // zeros times a non-finite weight are NaN: other tokens' columns stay as they were
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) acc[n][z] = (m >> (n * 8 + 2 * q + (z & 1))) & 1u ? acc[n][z] : before[n][z];
         c += k1 - k0;
     }
     for (int n = 0; n < (a.T + 7) / 8; ++n) {

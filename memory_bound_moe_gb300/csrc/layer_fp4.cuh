@@ -143,7 +143,14 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
             const uint64_t row = uint64_t(e) * H + mine;
             const Place4 p = {static_cast<const uint8_t*>(a.w2) + row * sh.rb + q * 64,
                               a.w2_scales + row * rs + q * (128 / WInfo<F>::kBlock), rows_ok};
+            float before[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) before[z] = acc[0][z];
             fp4_tile<F, NG>(acc, p, sh, from, to, smem, (c - c0) * 4, per, groups, F == kWNvfp4 ? 1.0f / a.w2_global[e] : 1.0f);
+            if constexpr (!kCompact) {   // zeros times a NaN weight are NaN: other tokens' columns stay as they were
+#pragma unroll
+                for (int z = 0; z < 4; ++z) acc[0][z] = (s.tokens[d] >> (2 * q + (z & 1))) & 1u ? acc[0][z] : before[z];
+            }
             c += to - from;
         }
         if constexpr (kCompact) {   // to the tokens' own columns
