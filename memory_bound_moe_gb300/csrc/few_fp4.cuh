@@ -12,7 +12,9 @@
 //    what smaller ones lose is under 2^-39 of the largest.
 //  - MXFP4: an E8M0 scale enters as 2^(X - Xmax + 13), Xmax the largest of the
 //    warp's blocks in a chunk of 512 k, and 2^(Xmax - 13) multiplies the sums. Where
-//    blocks lie more than 2^27 apart they take turns, each with its own Xmax.
+//    blocks lie more than 2^27 apart they take turns, each with its own Xmax; so
+//    they do where the powers of two for x and for the weights have a product
+//    that is no float32.
 //  - NVFP4: E4M3 scales and their products with E2M1 are within f16's range.
 //
 // Work. Next to the loads what bounds it is the arithmetic logic pipe: 16 lanes
@@ -67,7 +69,8 @@ constexpr uint32_t kChunkK = 512;   // k per chunk
 constexpr uint32_t kUnits = 88;                       // (group, step) units of x that shared memory holds
 constexpr uint32_t kUnit = 2048;                      // one unit: 8 tokens x 128 k, f16
 constexpr uint32_t kInvAt = kUnits * kUnit;           // the units' inverse powers of two, 8 each
-constexpr uint32_t kPartAt = kInvAt + kUnits * 32u;   // partial sums: [warp][tokens][16 rows]
+constexpr uint32_t kRangeAt = kInvAt + kUnits * 32u;  // bits of the least and the largest of them, as XRange
+constexpr uint32_t kPartAt = kRangeAt + 16u;          // partial sums: [warp][tokens][16 rows]
 
 template <int F, int NG>
 struct Fp4Block {
@@ -98,8 +101,8 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t scale, uint32_t
 }
 
 // One lane's 32 values of its token as f16, times a power of two shared by the
-// token's four lanes; returns the inverse of that power. Infinities and NaN
-// stay what they are.
+// token's four lanes; returns the inverse of that power (1 if all are zero).
+// Infinities and NaN stay what they are.
 __device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXPairs]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) { h[4 * i] = x[i].x; h[4 * i + 1] = x[i].y; h[4 * i + 2] = x[i].z; h[4 * i + 3] = x[i].w; }
@@ -110,7 +113,7 @@ __device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXP
     m = max(m >> 16, m & 0xffffu);
     m = max(m, __shfl_xor_sync(kFull, m, 1));
     m = max(m, __shfl_xor_sync(kFull, m, 2));
-    const uint32_t e = min(max(m >> 7, 15u), 254u);                  // biased exponent of the largest
+    const uint32_t e = m == 0u ? 141u : min(max(m >> 7, 15u), 254u);   // biased exponent of the largest
     const float scale = __uint_as_float((268u - e) << 23);           // 2^(14 - (e - 127))
 #pragma unroll
     for (int i = 0; i < kXPairs; ++i) {
@@ -120,6 +123,9 @@ __device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXP
     }
     return __uint_as_float((e - 14u) << 23);                         // 2^(e - 127 - 14)
 }
+
+// Whether a product of two powers of two is one, not 0 or infinity.
+__device__ __forceinline__ bool in_range(float p) { return p > 0.0f && p < __int_as_float(0x7f800000); }
 
 // 2^(x - 127 - 13), a subnormal float for x < 14.
 __device__ __forceinline__ float mxfp4_unit(uint32_t x) {
@@ -132,14 +138,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
+// The least and the largest inverse power of two among all units that the block
+// has staged so far: with these bits an MXFP4 chunk knows whether a product of
+// the factors for its weights and for x could leave float32. init by one thread,
+// before a barrier before the first stage_units.
+struct XRange {
+    uint32_t lo, hi;
+    __device__ __forceinline__ static XRange* at(uint8_t* smem) { return reinterpret_cast<XRange*>(smem + kRangeAt); }
+    __device__ __forceinline__ static void init(uint8_t* smem) {
+        at(smem)->lo = at(smem)->hi = __float_as_uint(1.0f);
+    }
+};
+
 // Units of x into shared memory, by all warps of the block: unit u is step u %
 // 4 of 8 rows; where(u, chunk) gives the lane group's row (NULL gives zeros)
 // and the chunk of k. For j = 0..3 a unit holds the 16 bytes that every lane
 // reads for word j of its granule. Two units' loads are in flight per warp.
-template <typename Where>
+template <int F, typename Where>
 __device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint32_t K, Where&& where) {
     const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
     const uint32_t W = blockDim.x / kWarp;
+    uint32_t lo = __float_as_uint(1.0f), hi = lo;
 #pragma unroll 1
     for (uint32_t u0 = threadIdx.x / kWarp; u0 < units; u0 += 2 * W) {
         uint4 x[2][4] = {};
@@ -165,6 +184,16 @@ __device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint3
 #pragma unroll
             for (int j = 0; j < 4; ++j) p[j * 32] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
             if (q == 0) reinterpret_cast<float*>(smem + kInvAt)[u * 8 + g] = inv;
+            lo = min(lo, __float_as_uint(inv));
+            hi = max(hi, __float_as_uint(inv));
+        }
+    }
+    if constexpr (F == kWMxfp4) {
+        lo = __reduce_min_sync(kFull, lo);
+        hi = __reduce_max_sync(kFull, hi);
+        if (lane == 0) {
+            atomicMin(&XRange::at(smem)->lo, lo);
+            atomicMax(&XRange::at(smem)->hi, hi);
         }
     }
 }
@@ -241,10 +270,10 @@ __device__ __forceinline__ void load_scales(WChunk4<F>& a, const Place4& at, con
     }
 }
 
-// MXFP4 blocks further apart than one window, with a NaN scale, or so small
-// that the factors' product could leave float32: turn by turn, each with the
-// largest scale among the blocks not yet added. Adds one group's products of a
-// chunk (its B fragments at xb, its inverse powers of two at inv) to acc.
+// MXFP4 blocks further apart than one window, with a NaN scale, or with factors
+// whose product is no float32: turn by turn, each with the largest scale among
+// the blocks not yet added. Adds one group's products of a chunk (its B
+// fragments at xb, its inverse powers of two at inv) to acc.
 __device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxfp4>& a, uint32_t xb, const float* inv, float f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -285,8 +314,10 @@ __device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxf
             }
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                const float fz = z & 1 ? f1 : f0;   // the smaller of the factors last: neither product leaves the range
-                acc[z] += fz <= 1.0f ? (c[z] * fz) * fx : (c[z] * fx) * fz;
+                const float fz = z & 1 ? f1 : f0, p = fz * fx;
+                // where the factors' product leaves float32 both are small or both large: one at a time, no step of
+                // c leaves it before the result does
+                acc[z] = in_range(p) ? fmaf(c[z], p, acc[z]) : acc[z] + (c[z] * fz) * fx;
             }
             todo = left;
         }
@@ -296,7 +327,17 @@ __device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxf
 // MXFP4: the largest scale of chunk c's blocks over the warp, and whether they
 // need turns. Granules that are cut off (their codes are zero) take the largest
 // finite scale for theirs: with another row's NaN they would be NaN as well.
-__device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole) {
+// ok: the largest scales whose factor has a float32 product with every one of x.
+struct TopRange {
+    uint32_t lo, n;   // lo .. lo + n
+    // 2^(i - 127) and 2^(top - 140) for i a bits' exponent: -149 <= i + top - 267 <= 127
+    __device__ __forceinline__ static TopRange of(uint8_t* smem) {
+        const uint32_t i0 = XRange::at(smem)->lo >> 23, i1 = XRange::at(smem)->hi >> 23;   // i0 <= 127 <= i1
+        const uint32_t lo = i0 < 118u ? 118u - i0 : 0u;
+        return {lo, min(254u, 394u - i1) - lo};
+    }
+};
+__device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole, TopRange ok) {
     uint32_t top = 0, low = 255u;
     if (!whole) {
         const uint32_t n = row_granules(sh.rb, c);
@@ -325,15 +366,16 @@ __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, 
             low = min(low, x);
         }
     top = __reduce_max_sync(kFull, top);
-    apart = __any_sync(kFull, low + 28u <= top) || top == 255u || top < 32u;
+    apart = __any_sync(kFull, low + 28u <= top) || top - ok.lo > ok.n;
     return top;
 }
 
 // Adds the chunks c0 .. c1 - 1 of a tile that need turns, and only those, to one
 // group's sums; x of chunk c0 begins at unit u0.
 __device__ __forceinline__ void mxfp4_apart_chunks(float* sums, const Place4* place, const Shape4* shape, uint32_t c0, uint32_t c1,
-                                                       uint8_t* smem, uint32_t u0, float f) {
+                                                   uint8_t* smem, uint32_t u0, float f) {
     const int lane = threadIdx.x % kWarp, q = lane % 4;
+    const TopRange ok = TopRange::of(smem);
     const Shape4 sh = *shape;
     Place4 p = *place;
     float acc[4] = {sums[0], sums[1], sums[2], sums[3]};
@@ -345,7 +387,7 @@ __device__ __forceinline__ void mxfp4_apart_chunks(float* sums, const Place4* pl
         WChunk4<kWMxfp4> a;
         bool apart;
         load_scales(a, p, sh, c, c < whole);
-        mxfp4_top(a, apart, p, sh, c, c < whole);
+        mxfp4_top(a, apart, p, sh, c, c < whole, ok);
         if (apart) {
             const uint32_t n = row_granules(sh.rb, c), u = u0 + (c - c0) * 4;
             load_rows(a.w, 0, p.w, sh.half_w, c < whole, p.rows, n, sh.whole > 0u);
@@ -427,6 +469,8 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], const Place4& p0, 
     }
     const uint32_t whole = __all_sync(kFull, p0.rows == 3u) ? sh.whole : 0u;   // chunks below it are whole
     bool some = false;   // MXFP4: whether chunks were left out, whose blocks need turns
+    TopRange ok = {};
+    if constexpr (F == kWMxfp4) ok = TopRange::of(smem);
     Place4 p = p0;
     p.w += c0 * 256u;
     p.s += c0 * (kChunkK / WInfo<F>::kBlock);
@@ -438,7 +482,7 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], const Place4& p0, 
     for (uint32_t c = c0; c < c1; ++c) {
         uint32_t top = 0;
         bool apart = false;
-        if constexpr (F == kWMxfp4) top = mxfp4_top(a, apart, p, sh, c, c < whole);
+        if constexpr (F == kWMxfp4) top = mxfp4_top(a, apart, p, sh, c, c < whole, ok);
         uint32_t sc[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)

@@ -45,13 +45,15 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) gemv_kernel(G
     const Place4 p = {a.codes + uint64_t(mine) * sh.rb + q * 64,
                       a.scales + uint64_t(mine) * row_scales<F>(a.K) + q * (128 / WInfo<F>::kBlock),
                       uint32_t(mine < a.N) | uint32_t(mine + 8 < a.N) << 1};
+    if (threadIdx.x == 0) XRange::init(smem);
+    __syncthreads();
     pdl_wait_and_release();
     float acc[NG][4] = {};
     const uint32_t slice = kUnits / 4 / groups;
     for (uint32_t s0 = c0; s0 < c1; s0 += slice) {
         const uint32_t n = min(slice, c1 - s0), per = n * 4;
         if (s0 > c0) __syncthreads();
-        stage_units(smem, per * groups, a.K, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
+        stage_units<F>(smem, per * groups, a.K, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
             const uint32_t gr = u / per, r = gr * 8 + g;
             chunk = s0 + (u - gr * per) / 4;
             return r < a.T ? a.x + uint64_t(r) * a.K : nullptr;

@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
     constexpr bool kCompact = NG > 1;   // B columns are the expert's own tokens
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ FewRoute s;
+    if (threadIdx.x == 0) XRange::init(smem);
     pdl_wait_and_release();
     route_few(a, s, blockIdx.x == 0);
     if (blockIdx.x == 0) save_route(static_cast<FewRouteCopy*>(a.route), s, a.T * a.k);
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
             const uint32_t n = min(slice, chunks - s0), per = n * 4;
             if (staged != (x * 4u + first / 8u) * 4096u + s0) {   // s0 < 2048
                 __syncthreads();
-                stage_units(smem, per * groups, H, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
+                stage_units<F>(smem, per * groups, H, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
                     const uint32_t gr = u / per, c = gr * 8 + g;
                     chunk = s0 + (u - gr * per) / 4;
                     if (kCompact) return int(c) < left ? a.x + uint64_t(s.row_t[s.off[x] + first + c]) * H : nullptr;
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
     float* s_mine = s_part + warp * part;
     if (kCompact)
         for (int o = lane; o < part; o += kWarp) s_mine[o] = 0.0f;
+    if (threadIdx.x == 0) XRange::init(smem);
     pdl_wait_and_release();
     load_route(s, static_cast<const FewRouteCopy*>(a.route), a.T * a.k);
     const Shape4 sh = fp4_shape<F>(8, I, a.w2);
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
         if (first == 0u) n = min(kUnits / 4 / groups, (kCompact ? min(c1, (d0 + 1) * chunks) : c1) - c0);
         const uint32_t per = n * 4;
         __syncthreads();
-        stage_units(smem, per * groups, I, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
+        stage_units<F>(smem, per * groups, I, [&](uint32_t u, uint32_t& chunk) -> const uint16_t* {
             const uint32_t gr = u / per, c = c0 + (u - gr * per) / 4, d = c / chunks, col = gr * 8 + g, m = s.tokens[d];
             chunk = c - d * chunks;
             if (kCompact ? int(col) >= left : !((m >> col) & 1u)) return nullptr;

@@ -1,0 +1,44 @@
+"""Products with 4-bit weights at the ends of the number range: very small and
+very large factors."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from few_reference import check_gemv, weights64
+from test_gpu_gemv_fp4 import make
+from test_gpu_layer import dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1, 4, 20])
+@pytest.mark.parametrize("ex,scale", [(-64, 67), (-100, 97), (-40, 40), (100, 34), (60, 60), (20, 200)])
+def test_mxfp4_factors_beyond_one_float(dev, T, ex, scale):  # noqa: F811
+    """x about 2^ex and weights about 2^(scale - 127): results that float32
+    holds, also where the powers of two behind x and behind the weights have a
+    product that it does not."""
+    from memory_bound_moe_gb300 import moe_gemv_fp4
+    N, K = 40, 1120
+    x, codes, scales, cd, _ = make(T, N, K, "mxfp4", dev, 51)
+    scales[:] = scale
+    x = (x.float() * 2.0 ** ex).to(torch.bfloat16)
+    y = moe_gemv_fp4(x, cd, torch.from_numpy(scales).to(dev), "mxfp4", out_dtype=torch.float32)
+    check_gemv(y, x, weights64(codes, scales, "mxfp4"), f"2^{ex}, scale {scale}")
+    # tokens of ordinary size beside them
+    if T > 1:
+        x[0] *= 2.0 ** -ex
+        y = moe_gemv_fp4(x, cd, torch.from_numpy(scales).to(dev), "mxfp4", out_dtype=torch.float32)
+        check_gemv(y, x, weights64(codes, scales, "mxfp4"), f"beside 2^{ex}, scale {scale}")
+
+
+@pytest.mark.parametrize("T", [2, 12])
+@pytest.mark.parametrize("ex", [40, 100, 127])
+def test_mxfp4_zero_weights_with_the_largest_scales(dev, T, ex):  # noqa: F811
+    """Blocks of zeros may have any finite scale byte; x large."""
+    from memory_bound_moe_gb300 import moe_gemv_fp4
+    N, K = 33, 1056
+    x = torch.full((T, K), 2.0 ** ex, dtype=torch.bfloat16, device=dev)
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.full((N, K // 32), 254, dtype=torch.uint8, device=dev)
+    assert (moe_gemv_fp4(x, codes, scales, "mxfp4", out_dtype=torch.float32) == 0).all()
