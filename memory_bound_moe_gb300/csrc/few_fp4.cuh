@@ -324,20 +324,22 @@ __device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxf
     }
 }
 
-// MXFP4: the largest scale of chunk c's blocks over the warp, and whether they
-// need turns. Granules that are cut off (their codes are zero) take the largest
-// finite scale for theirs: with another row's NaN they would be NaN as well.
-// ok: the largest scales whose factor has a float32 product with every one of x.
+// MXFP4: the scales lo .. lo + n whose factors 2^(top - 140) have a float32
+// product with every factor 2^(i - 127) of x: -149 <= i + top - 267 <= 127.
 struct TopRange {
-    uint32_t lo, n;   // lo .. lo + n
-    // 2^(i - 127) and 2^(top - 140) for i a bits' exponent: -149 <= i + top - 267 <= 127
+    uint32_t lo, n;
     __device__ __forceinline__ static TopRange of(uint8_t* smem) {
         const uint32_t i0 = XRange::at(smem)->lo >> 23, i1 = XRange::at(smem)->hi >> 23;   // i0 <= 127 <= i1
         const uint32_t lo = i0 < 118u ? 118u - i0 : 0u;
         return {lo, min(254u, 394u - i1) - lo};
     }
 };
-__device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole, TopRange ok) {
+
+// MXFP4: the largest scale of chunk c's blocks over the warp, and whether they
+// need turns. Granules that are cut off (their codes are zero) take the largest
+// finite scale for theirs: with another row's NaN they would be NaN as well.
+__device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole,
+                                              TopRange ok) {
     uint32_t top = 0, low = 255u;
     if (!whole) {
         const uint32_t n = row_granules(sh.rb, c);

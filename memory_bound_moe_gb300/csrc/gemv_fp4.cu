@@ -26,7 +26,7 @@ struct GemvArgs {
     void* y;
     uint32_t T, N, K;
     uint32_t chunks;   // of k in all
-    float inv_g;       // 1 / tensor scale (1 for MXFP4)
+    float g;           // tensor scale (NVFP4)
     int y_f32;
 };
 
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) gemv_kernel(G
     cluster_store(s_sum, T * rows, rows, rank, C, [&](int t, int i, float v) {
         const uint32_t row = row0 + i;
         if (row < a.N) {
-            v *= a.inv_g;
+            if constexpr (F == kWNvfp4) v /= a.g;   // 1 / g would round once more, and is infinite for a subnormal g
             const uint64_t to = uint64_t(t) * a.N + row;
             if (a.y_f32) static_cast<float*>(a.y)[to] = v;
             else static_cast<uint16_t*>(a.y)[to] = uint16_t(pack_bf16x2(v, 0.0f));
@@ -116,7 +116,7 @@ cudaError_t launch_gemv_fp4(const uint16_t* x, int T, int K, const uint8_t* code
     a.scales = scales;
     a.y = y;
     a.T = uint32_t(T); a.N = uint32_t(N); a.K = uint32_t(K);
-    a.inv_g = nvfp4 ? 1.0f / g : 1.0f;
+    a.g = g;
     a.y_f32 = y_f32 ? 1 : 0;
     return nvfp4 ? launch_f<kWNvfp4>(a, num_sms, stream) : launch_f<kWMxfp4>(a, num_sms, stream);
 }

@@ -1,7 +1,8 @@
 """Products with 4-bit weights at the ends of the number range: very small and
-very large factors."""
+very large factors and tensor scales."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -42,3 +43,18 @@ def test_mxfp4_zero_weights_with_the_largest_scales(dev, T, ex):  # noqa: F811
     codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=dev)
     scales = torch.full((N, K // 32), 254, dtype=torch.uint8, device=dev)
     assert (moe_gemv_fp4(x, codes, scales, "mxfp4", out_dtype=torch.float32) == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("g", [2e-39, 1e-44, 2.0 ** -126, 3e38])
+def test_nvfp4_every_allowed_tensor_scale(dev, T, g):  # noqa: F811
+    """Tensor scales whose reciprocal is no float32, or a subnormal one."""
+    from memory_bound_moe_gb300 import moe_gemv_fp4
+    g = float(np.float32(g))
+    N, K = 40, 288
+    x, codes, scales, cd, sd = make(T, N, K, "nvfp4", dev, 52)
+    codes[7] = 0
+    cd = torch.from_numpy(codes).to(dev)
+    x = (x.float() * (2.0 ** -60 if g < 1 else 2.0 ** 60)).to(torch.bfloat16)
+    y = moe_gemv_fp4(x, cd, sd, "nvfp4", g, out_dtype=torch.float32)
+    check_gemv(y, x, weights64(codes, scales, "nvfp4", g), f"g = {g}")
