@@ -274,10 +274,10 @@ __device__ __forceinline__ void load_scales(WChunk4<F>& a, const Place4& at, con
 // whose product is no float32: turn by turn, each with the largest scale among
 // the blocks not yet added. Adds one group's products of a chunk (its B
 // fragments at xb, its inverse powers of two at inv) to acc.
-__device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxfp4>& a, uint32_t xb, const float* inv, float f) {
+__device__ __forceinline__ void mxfp4_apart(float (&acc)[4], const WChunk4<kWMxfp4>& a, uint32_t xb, const float* inv) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float f0 = inv[i * 8] * f, f1 = inv[i * 8 + 1] * f;
+        const float f0 = inv[i * 8], f1 = inv[i * 8 + 1];
         uint32_t todo = 3u, sc[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) sc[k] = (a.s[k][i / 2] >> (8 * (i % 2))) & 255u;
@@ -375,7 +375,7 @@ __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, 
 // Adds the chunks c0 .. c1 - 1 of a tile that need turns, and only those, to one
 // group's sums; x of chunk c0 begins at unit u0.
 __device__ __forceinline__ void mxfp4_apart_chunks(float* sums, const Place4* place, const Shape4* shape, uint32_t c0, uint32_t c1,
-                                                   uint8_t* smem, uint32_t u0, float f) {
+                                                   uint8_t* smem, uint32_t u0) {
     const int lane = threadIdx.x % kWarp, q = lane % 4;
     const TopRange ok = TopRange::of(smem);
     const Shape4 sh = *shape;
@@ -395,7 +395,7 @@ __device__ __forceinline__ void mxfp4_apart_chunks(float* sums, const Place4* pl
             load_rows(a.w, 0, p.w, sh.half_w, c < whole, p.rows, n, sh.whole > 0u);
             load_rows(a.w, 1, p.w, sh.half_w, c < whole, p.rows, n, sh.whole > 0u);
             mxfp4_apart(acc, a, uint32_t(__cvta_generic_to_shared(smem)) + u * kUnit + lane * 16u,
-                        reinterpret_cast<const float*>(smem + kInvAt) + u * 8 + 2 * q, f);
+                        reinterpret_cast<const float*>(smem + kInvAt) + u * 8 + 2 * q);
         }
         p.w += 256;
         p.s += kChunkK / WInfo<kWMxfp4>::kBlock;
@@ -407,11 +407,12 @@ __device__ __forceinline__ void mxfp4_apart_chunks(float* sums, const Place4* pl
 // The products of step i of a chunk with the first `groups` groups of 8 tokens.
 // xb[n]: this lane's B fragments of group n in the chunk's first unit, inv[n]:
 // that unit's inverse powers of two of the lane's two tokens in C, 2 q and 2 q
-// + 1; f multiplies the sums, top as of mxfp4_top.
+// + 1; top as of mxfp4_top.
 template <int F, int NG>
 __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& a, const uint32_t (&sc)[2][2],
-                                         int i, const uint32_t (&xb)[NG], const float* (&inv)[NG], int groups, float f,
+                                         int i, const uint32_t (&xb)[NG], const float* (&inv)[NG], int groups,
                                          uint32_t top) {
+    float f = 1.0f;     // multiplies the sums
     uint32_t s[2][2];   // f16 scale in both halves: [row g or g + 8][k 0..15 or 16..31 of the granule]
     if constexpr (F == kWNvfp4) {
 #pragma unroll
@@ -423,7 +424,7 @@ __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& 
             s[k][1] = __byte_perm(v, v, 0x3232);
         }
     } else {
-        f *= mxfp4_unit(top);
+        f = mxfp4_unit(top);
         const uint32_t shift = (28u - top) * 0x04000400u;   // biased f16 exponent X - top + 28, in both halves
 #pragma unroll
         for (int k = 0; k < 2; ++k) s[k][0] = s[k][1] = __byte_perm(sc[k][i / 2], 0, 0x4440 + i % 2) * 0x04000400u + shift;
@@ -458,7 +459,7 @@ __device__ __forceinline__ void fp4_step(float (&acc)[NG][4], const WChunk4<F>& 
 // shared memory, each group's `group_units` behind the one before.
 template <int F, int NG>
 __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], const Place4& p0, const Shape4& sh, uint32_t c0, uint32_t c1,
-                                         uint8_t* smem, uint32_t u0, uint32_t group_units, int groups, float f) {
+                                         uint8_t* smem, uint32_t u0, uint32_t group_units, int groups) {
     if (c0 >= c1) return;
     const int lane = threadIdx.x % kWarp, q = lane % 4;
     uint32_t xb[NG];
@@ -496,13 +497,13 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], const Place4& p0, 
         if (more) load_scales(a, p, sh, c + 1, c + 1 < whole);
         some |= apart;
         if (!apart) {
-            fp4_step<F, NG>(acc, a, sc, 0, xb, inv, groups, f, top);
-            fp4_step<F, NG>(acc, a, sc, 1, xb, inv, groups, f, top);
+            fp4_step<F, NG>(acc, a, sc, 0, xb, inv, groups, top);
+            fp4_step<F, NG>(acc, a, sc, 1, xb, inv, groups, top);
         }
         if (more) load_rows(a.w, 0, p.w, sh.half_w, c + 1 < whole, p.rows, row_granules(sh.rb, c + 1), sh.whole > 0u);
         if (!apart) {
-            fp4_step<F, NG>(acc, a, sc, 2, xb, inv, groups, f, top);
-            fp4_step<F, NG>(acc, a, sc, 3, xb, inv, groups, f, top);
+            fp4_step<F, NG>(acc, a, sc, 2, xb, inv, groups, top);
+            fp4_step<F, NG>(acc, a, sc, 3, xb, inv, groups, top);
         }
         if (more) load_rows(a.w, 1, p.w, sh.half_w, c + 1 < whole, p.rows, row_granules(sh.rb, c + 1), sh.whole > 0u);
 #pragma unroll
@@ -519,7 +520,7 @@ __device__ __forceinline__ void fp4_tile(float (&acc)[NG][4], const Place4& p0, 
                 float v[4] = {acc[n][0], acc[n][1], acc[n][2], acc[n][3]};
                 const Place4 place = p0;
                 const Shape4 shape = sh;
-                mxfp4_apart_chunks(v, &place, &shape, c0, c1, smem, u0 + n * group_units, f);
+                mxfp4_apart_chunks(v, &place, &shape, c0, c1, smem, u0 + n * group_units);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) acc[n][z] = v[z];
             }

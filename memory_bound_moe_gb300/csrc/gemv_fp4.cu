@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) gemv_kernel(G
         });
         __syncthreads();
         const uint32_t k0 = n * ks / KS, k1 = n * (ks + 1) / KS;
-        fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups, 1.0f);
+        fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups);
     }
     for (int n = 0; n < groups; ++n) {
         __syncthreads();

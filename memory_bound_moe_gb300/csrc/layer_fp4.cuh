@@ -57,7 +57,6 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
         const uint64_t row = uint64_t(e) * 2 * I + j0 + g;
         const Place4 p = {static_cast<const uint8_t*>(a.w13) + row * sh.rb + q * 64,
                           a.w13_scales + row * rs + q * (128 / WInfo<F>::kBlock), 3u};
-        const float f = F == kWNvfp4 ? 1.0f / a.w13_global[e] : 1.0f;
         const uint32_t slice = kUnits / 4 / groups;
         float acc[NG][4] = {};
         for (uint32_t s0 = 0; s0 < chunks; s0 += slice) {
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
                 staged = (x * 4u + first / 8u) * 4096u + s0;
             }
             const uint32_t k0 = n * ks / KS, k1 = n * (ks + 1) / KS;
-            if (t < stop) fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups, f);
+            if (t < stop) fp4_tile<F, NG>(acc, p, sh, s0 + k0, s0 + k1, smem, k0 * 4, per, groups);
         }
         // a pass over the block's tiles of the expert, then the next 8 NG tokens or the next expert
         const uint32_t tokens0 = first;
@@ -93,8 +92,14 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
                 const int c = o / 8, col = int(tokens0) + n * 8 + c;
                 if (kCompact ? col >= __popc(m) : !((m >> col) & 1u)) continue;
                 const uint32_t to = s.off[d] + (kCompact ? col : __popc(m & ((1u << col) - 1u)));
-                const float gate = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8), up = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8 + 8);
-                a.act[uint64_t(to) * I + j0 + o % 8] = uint16_t(pack_bf16x2(s.row_w[to] * (silu(gate) * up), 0.0f));
+                float gate = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8), up = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8 + 8);
+                if constexpr (F == kWNvfp4) {
+                    gate /= a.w13_global[e];
+                    up /= a.w13_global[e];
+                }
+                float v = s.row_w[to] * (silu(gate) * up);
+                if constexpr (F == kWNvfp4) v /= a.w2_global[e];   // fc2 sums over experts of different scales
+                a.act[uint64_t(to) * I + j0 + o % 8] = uint16_t(pack_bf16x2(v, 0.0f));
             }
         }
     }
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
             float before[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) before[z] = acc[0][z];
-            fp4_tile<F, NG>(acc, p, sh, from, to, smem, (c - c0) * 4, per, groups, F == kWNvfp4 ? 1.0f / a.w2_global[e] : 1.0f);
+            fp4_tile<F, NG>(acc, p, sh, from, to, smem, (c - c0) * 4, per, groups);
             if constexpr (!kCompact) {   // zeros times a NaN weight are NaN: other tokens' columns stay as they were
 #pragma unroll
                 for (int z = 0; z < 4; ++z) acc[0][z] = (s.tokens[d] >> (2 * q + (z & 1))) & 1u ? acc[0][z] : before[z];

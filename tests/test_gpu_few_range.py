@@ -8,7 +8,7 @@ import torch
 
 from few_reference import check_gemv, weights64
 from test_gpu_gemv_fp4 import make
-from test_gpu_layer import dev  # noqa: F401
+from test_gpu_layer import Layer, dev, run_and_check, tokens  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,17 @@ def test_nvfp4_every_allowed_tensor_scale(dev, T, g):  # noqa: F811
     x = (x.float() * (2.0 ** -60 if g < 1 else 2.0 ** 60)).to(torch.bfloat16)
     y = moe_gemv_fp4(x, cd, sd, "nvfp4", g, out_dtype=torch.float32)
     check_gemv(y, x, weights64(codes, scales, "nvfp4", g), f"g = {g}")
+
+
+@pytest.mark.parametrize("T", [2, 12])
+@pytest.mark.parametrize("g13,g2", [(2e-39, 1e30), (3e-42, 1e35), (3e38, 2.0 ** -126)])
+def test_layer_nvfp4_extreme_tensor_scales(dev, T, g13, g2):  # noqa: F811
+    """Weights and x so far apart that the sums before the division by the
+    tensor scale, or its reciprocal, lie at an end of float32."""
+    E, H, I, k = 4, 96, 64, 2
+    layer = Layer(E, H, I, "nvfp4", dev, 53)
+    layer.g = [np.full(E, g13, np.float32), np.full(E, g2, np.float32)]
+    layer.gd = [torch.from_numpy(g).to(dev) for g in layer.g]
+    logits, x = tokens(T, E, H, dev, 54)
+    x = (x.float() * (2.0 ** -120 if g13 < 1 else 2.0 ** 100)).to(torch.bfloat16)
+    run_and_check(layer, logits, x, k, True, f"g = {g13}, {g2}")
