@@ -424,8 +424,8 @@ moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residu
  * != 0, float32 (logits). The weights' values are exact; a scale byte that
  * encodes NaN makes its block NaN. x enters in f16 times a power of two per
  * token and 128 k: exact down to 2^-32 of the largest of those 128 values;
- * smaller ones lose at most 2^-39 of it. (The same for x and a in
- * moe_layer_fp4.)
+ * smaller ones lose at most 2^-39 of it. (The same for x in moe_layer_fp4.)
+ * NVFP4 sums are divided by global_scale once they are complete.
  * T <= MOE_FEW_MAX_TOKENS and K <= 2^20 (MOE_ERR_UNSUPPORTED); K a multiple
  * of 32, x, codes and scales 16-byte, y 4-byte aligned (MOE_ERR_MISALIGNED);
  * N any positive number. Results do not depend on timing; needs no workspace.
@@ -446,7 +446,9 @@ moe_status_t moe_gemv_fp4(const moe_bf16_t* x, int64_t T, int K, const uint8_t* 
  *   a[t, j, :] = bf16_rn( w[t, j] * silu(W13[e, 0..I) x_t) * (W13[e, I..2I) x_t) )
  *   out[t, :]  = bf16_rn( sum_j W2[e] a[t, j, :] ),   e = ids[t, j]
  * with float32 products, sums and silu (the weight enters before a's one
- * rounding; a stays in the workspace). logits [T, E] float32, x [T, H],
+ * rounding; a stays in the workspace). moe_layer_fp4 rounds a to the 11 bits of
+ * f16 in place of bfloat16's 8 (values below 2^-28 of the largest of 128 to
+ * 2^-38 of that). logits [T, E] float32, x [T, H],
  * w13 [E, 2I, H] (gate rows first), w2 [E, H, I], out [T, H], bfloat16.
  * topk_ids [T, k] and topk_weights [T, k] get the routing of moe_route, bit
  * for bit; either may be NULL.
@@ -455,7 +457,7 @@ moe_status_t moe_gemv_fp4(const moe_bf16_t* x, int64_t T, int K, const uint8_t* 
  * [E, 2I, H/2] and [E, H, I/2], scales [E, 2I, H/b] and [E, H, I/b] with
  * b = 32 (MXFP4) or 16 (NVFP4), and for NVFP4 one float32 tensor scale per
  * expert and matrix in device memory, w13_global [E] and w2_global [E] (finite
- * and positive; NULL for MXFP4).
+ * and positive, a / w2_global within float32; NULL for MXFP4).
  *
  * Weights of experts that no token chose are not read. Logits are assumed
  * finite (others: unspecified, in-bounds picks). Limits: T <=

@@ -594,10 +594,11 @@ moe_status_t check_layer_sizes(int64_t T, int E, int k, int H, int I) {
     return MOE_OK;
 }
 
-// The activation [T k, I] in bfloat16 (a multiple of 16 bytes), then the
-// routing that fc1 leaves for fc2.
+// The activation [T k, I] in 16 bits, an exponent for every 8 of it (4-bit
+// weights; padded to whole 16 bytes), then the routing that fc1 leaves for fc2.
 uint64_t layer_act(int64_t T, int k, int I) { return 2 * uint64_t(T) * uint64_t(k) * uint64_t(I); }
-uint64_t layer_workspace(int64_t T, int k, int I) { return layer_act(T, k, I) + moe::kFewRouteBytes; }
+uint64_t layer_exps(int64_t T, int k, int I) { return (layer_act(T, k, I) / 16 + 15) / 16 * 16; }
+uint64_t layer_workspace(int64_t T, int k, int I) { return layer_act(T, k, I) + layer_exps(T, k, I) + moe::kFewRouteBytes; }
 
 using LayerLaunch = cudaError_t (*)(const moe::LayerArgs&, int, cudaStream_t);
 
@@ -626,7 +627,8 @@ moe_status_t run_layer(moe::LayerArgs& a, LayerLaunch launch, const float* logit
     a.topk_ids = topk_ids;
     a.topk_weights = topk_weights;
     a.act = static_cast<uint16_t*>(workspace);
-    a.route = static_cast<uint8_t*>(workspace) + layer_act(T, k, I);
+    a.act_exps = static_cast<uint8_t*>(workspace) + layer_act(T, k, I);
+    a.route = a.act_exps + layer_exps(T, k, I);
     a.T = int(T); a.E = E; a.k = k; a.renorm = renorm ? 1 : 0; a.H = H; a.I = I;
     return from_cuda(launch(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -10,6 +10,12 @@
 //    two that brings their largest into [2^14, 2^15), and the step's sums by
 //    its inverse. A value 2^-32 of the step's largest still keeps its 8 bits;
 //    what smaller ones lose is under 2^-39 of the largest.
+//  - a, the layer's activation: fc1 leaves it as f16 with an exponent per 8
+//    columns, its largest in [2^14, 2^15) as well; fc2 takes a step's values to
+//    the largest exponent among them. That keeps 11 bits in 2.1 bytes. bfloat16
+//    would leave 8, a second rounding as large as the result's own; float32 has
+//    twice the bytes. (T=32, E=8, k=2, H=4096, I=14336: NVFP4 253 us, MXFP4 360;
+//    249 and 356 in bfloat16, 263 and 370 in float32.)
 //  - MXFP4: an E8M0 scale enters as 2^(X - Xmax + 13), Xmax the largest of the
 //    warp's blocks in a chunk of 512 k, and 2^(Xmax - 13) multiplies the sums. Where
 //    blocks lie more than 2^27 apart they take turns, each with its own Xmax; so
@@ -124,6 +130,44 @@ __device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXP
     return __uint_as_float((e - 14u) << 23);                         // 2^(e - 127 - 14)
 }
 
+__device__ __forceinline__ uint16_t f16_bits(float v) {
+    uint16_t r;
+    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(v));
+    return r;
+}
+
+// Four f16 pairs times 2^-d, d <= 14.
+__device__ __forceinline__ void scale_f16(uint32_t* h, uint32_t d) {
+    const uint32_t m = 0x3c003c00u - d * 0x04000400u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(m));
+}
+
+// The same of 32 activations, which are f16 already, the 8 of x[z] with the
+// exponent in byte z of exps (0: all are zero).
+__device__ __forceinline__ float a_to_f16(const uint4 (&x)[4], uint32_t exps, uint32_t (&h)[kXPairs]) {
+    uint32_t d[4], top = 0, far = 0;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        d[z] = __byte_perm(exps, 0, 0x4440 + z);
+        top = max(top, d[z]);
+    }
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        d[z] = top - d[z];
+        far = max(far, d[z]);
+        h[4 * z] = x[z].x; h[4 * z + 1] = x[z].y; h[4 * z + 2] = x[z].z; h[4 * z + 3] = x[z].w;
+        scale_f16(h + 4 * z, min(d[z], 14u));
+    }
+#pragma unroll 1
+    for (uint32_t s = 14; s < min(far, 42u); s += 14)   // rare; below 2^-42 nothing is left of f16
+#pragma unroll
+        for (int z = 0; z < 4; ++z) scale_f16(h + 4 * z, min(d[z] - min(d[z], s), 14u));
+    return top == 0u ? 1.0f : __uint_as_float((top - 14u) << 23);
+}
+
 // Whether a product of two powers of two is one, not 0 or infinity.
 __device__ __forceinline__ bool in_range(float p) { return p > 0.0f && p < __int_as_float(0x7f800000); }
 
@@ -154,14 +198,17 @@ struct XRange {
 // 4 of 8 rows; where(u, chunk) gives the lane group's row (NULL gives zeros)
 // and the chunk of k. For j = 0..3 a unit holds the 16 bytes that every lane
 // reads for word j of its granule. Two units' loads are in flight per warp.
+// The rows are bfloat16, or activations (act and exps: the whole arrays).
 template <int F, typename Where>
-__device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint32_t K, Where&& where) {
+__device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint32_t K, Where&& where, const uint16_t* act = nullptr,
+                                            const uint8_t* exps = nullptr) {
     const int lane = threadIdx.x % kWarp, g = lane / 4, q = lane % 4;
     const uint32_t W = blockDim.x / kWarp;
     uint32_t lo = __float_as_uint(1.0f), hi = lo;
 #pragma unroll 1
     for (uint32_t u0 = threadIdx.x / kWarp; u0 < units; u0 += 2 * W) {
         uint4 x[2][4] = {};
+        uint32_t ex[2] = {};
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k) {
             const uint32_t u = u0 + k * W;
@@ -172,6 +219,7 @@ __device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint3
             if (row != nullptr && k0 < K) {
 #pragma unroll
                 for (int z = 0; z < 4; ++z) x[k][z] = __ldg(reinterpret_cast<const uint4*>(row + k0) + z);
+                if (exps != nullptr) ex[k] = __ldg(reinterpret_cast<const uint32_t*>(exps + uint64_t(row + k0 - act) / 8));
             }
         }
 #pragma unroll
@@ -179,7 +227,7 @@ __device__ __forceinline__ void stage_units(uint8_t* smem, uint32_t units, uint3
             const uint32_t u = u0 + k * W;
             if (u >= units) break;
             uint32_t h[kXPairs];
-            const float inv = x_to_f16(x[k], h);
+            const float inv = exps != nullptr ? a_to_f16(x[k], ex[k], h) : x_to_f16(x[k], h);
             uint4* p = reinterpret_cast<uint4*>(smem + u * kUnit) + lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j) p[j * 32] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);

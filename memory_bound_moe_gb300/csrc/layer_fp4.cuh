@@ -1,6 +1,7 @@
 // Kernels of the MoE layer for a few tokens with 4-bit weights, on the inner
 // loop of few_fp4.cuh. See layer_bf16.cu for what fc1 and fc2 compute and how
-// the batch is routed. Up to 8 tokens the B columns are the tokens themselves;
+// the batch is routed; the activation is f16 here, with exponents of its own, and
+// with NVFP4 already divided by the tensor scale of the expert's w2. Up to 8 tokens the B columns are the tokens themselves;
 // above, they are the expert's own tokens, 8 to a group and two groups to a
 // pass: an expert with more than 16 of at most 32 tokens takes a second pass
 // over its weights (from L2 or not), which is rare enough that two more groups'
@@ -99,7 +100,14 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
                 }
                 float v = s.row_w[to] * (silu(gate) * up);
                 if constexpr (F == kWNvfp4) v /= a.w2_global[e];   // fc2 sums over experts of different scales
-                a.act[uint64_t(to) * I + j0 + o % 8] = uint16_t(pack_bf16x2(v, 0.0f));
+                // as f16 times a power of two of the token's 8 columns, which lie in 8 neighbouring lanes
+                float most = fabsf(v);
+#pragma unroll
+                for (int i = 1; i < 8; i <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffu << (lane & 24), most, i));
+                const uint32_t ex = most > 0.0f ? min(max(__float_as_uint(most) >> 23, 15u), 254u) : 0u;
+                const uint64_t at = uint64_t(to) * I + j0;
+                a.act[at + o % 8] = f16_bits(ex > 0u ? v * __uint_as_float((268u - ex) << 23) : v);
+                if (o % 8 == 0) a.act_exps[at / 8] = uint8_t(ex);
             }
         }
     }
@@ -141,7 +149,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc2_fp4_kerne
             chunk = c - d * chunks;
             if (kCompact ? int(col) >= left : !((m >> col) & 1u)) return nullptr;
             return a.act + uint64_t(s.off[d] + (kCompact ? first + col : uint32_t(__popc(m & ((1u << col) - 1u))))) * I;
-        });
+        }, a.act, a.act_exps);
         __syncthreads();
         // this warp's share, expert by expert
         const uint32_t k1 = c0 + n * (ks + 1) / KS;

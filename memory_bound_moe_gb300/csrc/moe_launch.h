@@ -108,7 +108,8 @@ struct LayerArgs {
     uint16_t* out;
     int32_t* topk_ids;           // may be NULL
     float* topk_weights;         // may be NULL
-    uint16_t* act;               // workspace [T*k, I]
+    uint16_t* act;               // workspace [T*k, I]: bfloat16; f16 for 4-bit weights
+    uint8_t* act_exps;           // workspace [T*k, I/8] (4-bit weights): exponents of 8 columns' f16
     void* route;                 // workspace, kFewRouteBytes
     int T, E, k, renorm, H, I;
 };
