@@ -423,7 +423,7 @@ moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residu
  * (NVFP4), row-major. y [T, N], bfloat16 (rounded once) or, with y_float32
  * != 0, float32 (logits). The weights' values are exact; a scale byte that
  * encodes NaN makes its block NaN. x enters in f16 times a power of two per
- * token and 128 k: exact down to 2^-32 of the largest of those 128 values;
+ * token and 128 k: exact down to 2^-31 of the largest of those 128 values;
  * smaller ones lose at most 2^-39 of it. (The same for x in moe_layer_fp4.)
  * NVFP4 sums are divided by global_scale once they are complete.
  * T <= MOE_FEW_MAX_TOKENS and K <= 2^20 (MOE_ERR_UNSUPPORTED); K a multiple

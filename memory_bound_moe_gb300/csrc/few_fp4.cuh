@@ -8,8 +8,9 @@
 // values:
 //  - x: each token's values of one step (128 k) are multiplied by the power of
 //    two that brings their largest into [2^14, 2^15), and the step's sums by
-//    its inverse. A value 2^-32 of the step's largest still keeps its 8 bits;
-//    what smaller ones lose is under 2^-39 of the largest.
+//    its inverse. A value 2^-31 of the step's largest still keeps its 8 bits: it
+//    is 2^-17 or more, and f16's last step is 2^-24. What smaller ones lose is at
+//    most 2^-39 of the largest.
 //  - a, the layer's activation: fc1 leaves it as f16 with an exponent per 8
 //    columns, its largest in [2^14, 2^15) as well; fc2 takes a step's values to
 //    the largest exponent among them. That keeps 11 bits in 2.1 bytes. bfloat16

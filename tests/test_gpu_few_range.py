@@ -1,13 +1,13 @@
 """Products with 4-bit weights at the ends of the number range: very small and
-very large factors and tensor scales."""
+very large factors and tensor scales, and the border of what x keeps."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 import torch
 
-from few_reference import check_gemv, weights64
-from test_gpu_gemv_fp4 import make
+from few_reference import BLOCK, check_gemv, weights64
+from test_gpu_gemv_fp4 import FMTS, make
 from test_gpu_layer import Layer, dev, run_and_check, tokens  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -72,3 +72,24 @@ def test_layer_nvfp4_extreme_tensor_scales(dev, T, g13, g2):  # noqa: F811
     logits, x = tokens(T, E, H, dev, 54)
     x = (x.float() * (2.0 ** -120 if g13 < 1 else 2.0 ** 100)).to(torch.bfloat16)
     run_and_check(layer, logits, x, k, True, f"g = {g13}, {g2}")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("big", [1.0, 1.9921875])
+def test_what_x_keeps_beside_a_large_value(dev, fmt, big):  # noqa: F811
+    """Beside `big`, a value down to 2^-31 of it keeps all its bits; one
+    smaller loses at most 2^-39 of it."""
+    from memory_bound_moe_gb300 import moe_gemv_fp4
+    K = 128
+    one = 0x38 if fmt == "nvfp4" else 127
+    scales = torch.full((1, K // BLOCK[fmt]), one, dtype=torch.uint8, device=dev)
+    codes = torch.zeros((1, K // 2), dtype=torch.uint8, device=dev)
+    codes[0, 5] = 0x20                                          # weight 11 is 1, weight 100 is 0
+    for e in (-20, -30, -31, -32, -33, -36, -40):
+        for m in (1.0, 1.0078125, 1.5, 1.9921875):              # 8 significant bits
+            x = torch.zeros((1, K), dtype=torch.bfloat16)
+            x[0, 100], x[0, 11] = big, m * 2.0 ** e
+            y = float(moe_gemv_fp4(x.to(dev), codes, scales, fmt, out_dtype=torch.float32))
+            if m * 2.0 ** e >= big * 2.0 ** -31:
+                assert y == float(x[0, 11]), (e, m)
+            assert abs(y - float(x[0, 11])) <= big * 2.0 ** -39, (e, m)
