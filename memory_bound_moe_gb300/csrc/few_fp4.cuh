@@ -386,7 +386,7 @@ struct TopRange {
 
 // MXFP4: the largest scale of chunk c's blocks over the warp, and whether they
 // need turns. Granules that are cut off (their codes are zero) take the largest
-// finite scale for theirs: with another row's NaN they would be NaN as well.
+// scale for theirs, but not NaN (255), which would make them NaN as well.
 __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, const Place4& p, const Shape4& sh, uint32_t c, bool whole,
                                               TopRange ok) {
     uint32_t top = 0, low = 255u;
@@ -395,11 +395,8 @@ __device__ __forceinline__ uint32_t mxfp4_top(WChunk4<kWMxfp4>& a, bool& apart, 
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t x = (a.s[h][i / 2] >> (8 * (i % 2))) & 255u;
-                if (x != 255u) top = max(top, x);
-            }
-        top = __reduce_max_sync(kFull, top);
+            for (int i = 0; i < 4; ++i) top = max(top, (a.s[h][i / 2] >> (8 * (i % 2))) & 255u);
+        top = min(__reduce_max_sync(kFull, top), 254u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t m = (p.rows >> h) & 1u ? n : 0u;
