@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
         const uint64_t row = uint64_t(e) * 2 * I + j0 + g;
         const Place4 p = {static_cast<const uint8_t*>(a.w13) + row * sh.rb + q * 64,
                           a.w13_scales + row * rs + q * (128 / WInfo<F>::kBlock), 3u};
+        const float g13 = F == kWNvfp4 ? a.w13_global[e] : 1.0f, g2 = F == kWNvfp4 ? a.w2_global[e] : 1.0f;
         const uint32_t slice = kUnits / 4 / groups;
         float acc[NG][4] = {};
         for (uint32_t s0 = 0; s0 < chunks; s0 += slice) {
@@ -95,11 +96,11 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
                 const uint32_t to = s.off[d] + (kCompact ? col : __popc(m & ((1u << col) - 1u)));
                 float gate = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8), up = sum_splits(s_part, rg, KS, 128, c * 16 + o % 8 + 8);
                 if constexpr (F == kWNvfp4) {
-                    gate /= a.w13_global[e];
-                    up /= a.w13_global[e];
+                    gate /= g13;
+                    up /= g13;
                 }
                 float v = s.row_w[to] * (silu(gate) * up);
-                if constexpr (F == kWNvfp4) v /= a.w2_global[e];   // fc2 sums over experts of different scales
+                if constexpr (F == kWNvfp4) v /= g2;   // fc2 sums over experts of different scales
                 // as f16 times a power of two of the token's 8 columns, which lie in 8 neighbouring lanes
                 float most = fabsf(v);
 #pragma unroll
