@@ -38,7 +38,8 @@
  *   - A zero-sized batch (T = 0 or rows = 0) is valid; pointers of empty
  *     arrays may then be NULL.
  *   - The functions are thread-safe and keep no mutable global state apart
- *     from a per-device cache of the SM count. The one exception is
+ *     from per-device caches of what the device offers (the SM count, clusters
+ *     that fit at once, granted shared memory). The one exception is
  *     moe_route_static, whose calls share one static scratch array and so
  *     must not overlap on the GPU (see its comment below).
  *
@@ -393,7 +394,9 @@ moe_status_t moe_qk_rmsnorm(moe_bf16_t* q, moe_bf16_t* k, int64_t T, int num_q_h
  *   out[t, :] = bf16_rn( (weight + weight_bias) * (h * r) ),
  *   r = 1 / sqrt(sum(h^2) / H + eps)   (float32)
  * The norm is taken of the float32 sum, before the residual is rounded. The
- * sum of squares is float32: rows with |h| above about 1e19 overflow it.
+ * sum of squares is float32: rows with |h| above about 1e19 overflow it, and
+ * with eps = 0 rows whose squares all vanish in it (|h| below about 1e-23, zero
+ * rows too) give infinities or NaN.
  * x, residual, out, residual_out [T, H], weight [H]: bfloat16, 16-byte
  * aligned, H a multiple of 8. residual_out may be NULL (not stored), must be
  * NULL if residual is, and may be residual itself (in place); apart from
@@ -425,6 +428,7 @@ moe_status_t moe_add_rmsnorm_mxfp8(const moe_bf16_t* x, const moe_bf16_t* residu
  * encodes NaN makes its block NaN. x enters in f16 times a power of two per
  * token and 128 k: exact down to 2^-31 of the largest of those 128 values;
  * smaller ones lose at most 2^-39 of it. (The same for x in moe_layer_fp4.)
+ * Non-finite values of x make their own token's results infinite or NaN.
  * NVFP4 sums are divided by global_scale once they are complete.
  * T <= MOE_FEW_MAX_TOKENS and K <= 2^20 (MOE_ERR_UNSUPPORTED); K a multiple
  * of 32, x, codes and scales 16-byte, y 4-byte aligned (MOE_ERR_MISALIGNED);
@@ -459,7 +463,8 @@ moe_status_t moe_gemv_fp4(const moe_bf16_t* x, int64_t T, int K, const uint8_t* 
  * expert and matrix in device memory, w13_global [E] and w2_global [E] (finite
  * and positive, a / w2_global within float32; NULL for MXFP4).
  *
- * Weights of experts that no token chose are not read. Logits are assumed
+ * Weights of experts that no token chose are not read, and non-finite ones of
+ * an expert reach the tokens that chose it and no others. Logits are assumed
  * finite (others: unspecified, in-bounds picks). Limits: T <=
  * MOE_FEW_MAX_TOKENS, H and I <= 2^20 (MOE_ERR_UNSUPPORTED) and multiples of
  * 8, of 32 for 4-bit weights (MOE_ERR_MISALIGNED); all weights and scales

@@ -15,7 +15,7 @@
 //    columns, its largest in [2^14, 2^15) as well; fc2 takes a step's values to
 //    the largest exponent among them. That keeps 11 bits in 2.1 bytes. bfloat16
 //    would leave 8, a second rounding as large as the result's own; float32 has
-//    twice the bytes. (T=32, E=8, k=2, H=4096, I=14336: NVFP4 253 us, MXFP4 360;
+//    twice the bytes. (T=32, E=8, k=2, H=4096, I=14336: NVFP4 252 us, MXFP4 358;
 //    249 and 356 in bfloat16, 263 and 370 in float32.)
 //  - MXFP4: an E8M0 scale enters as 2^(X - Xmax + 13), Xmax the largest of the
 //    warp's blocks in a chunk of 512 k, and 2^(Xmax - 13) multiplies the sums. Where
@@ -131,9 +131,16 @@ __device__ __forceinline__ float x_to_f16(const uint4 (&x)[4], uint32_t (&h)[kXP
     return __uint_as_float((e - 14u) << 23);                         // 2^(e - 127 - 14)
 }
 
-__device__ __forceinline__ uint16_t f16_bits(float v) {
+// A column's activation v as fc1 leaves it: f16, times the power of two that
+// brings the largest of its 8 columns, in this and its 7 neighbouring lanes, into
+// [2^14, 2^15); exponent: that largest's, biased, or 0 where all are zero or NaN.
+__device__ __forceinline__ uint16_t act_to_f16(float v, uint32_t& exponent) {
+    float most = fabsf(v);
+#pragma unroll
+    for (int i = 1; i < 8; i <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffu << (threadIdx.x & 24), most, i));
+    exponent = most > 0.0f ? min(max(__float_as_uint(most) >> 23, 15u), 254u) : 0u;
     uint16_t r;
-    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(v));
+    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(exponent > 0u ? v * __uint_as_float((268u - exponent) << 23) : v));
     return r;
 }
 
@@ -144,8 +151,8 @@ __device__ __forceinline__ void scale_f16(uint32_t* h, uint32_t d) {
     for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(m));
 }
 
-// The same of 32 activations, which are f16 already, the 8 of x[z] with the
-// exponent in byte z of exps (0: all are zero).
+// x_to_f16 of 32 activations as act_to_f16 left them, the 8 of x[z] with the
+// exponent in byte z of exps: all to the largest exponent of the four lanes.
 __device__ __forceinline__ float a_to_f16(const uint4 (&x)[4], uint32_t exps, uint32_t (&h)[kXPairs]) {
     uint32_t d[4], top = 0, far = 0;
 #pragma unroll

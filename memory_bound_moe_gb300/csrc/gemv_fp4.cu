@@ -8,10 +8,11 @@
 // in shared memory, then through distributed shared memory, always in the same
 // order: results do not depend on timing.
 //
-// Measured on GB300 in graphs: T=7, N=28672, K=4096 NVFP4 19.3 us (3.4 TB/s of
-// weights, half the copy rate, bound by the loop's instructions); T=16, N=4096,
-// K=7168 NVFP4 12.7 us, T=32, N=5760, K=2880 MXFP4 14.6 us, T=1, N=2048, K=768
-// MXFP4 4.1 us (latency: launch, x to f16, one or two chunks per warp, sums).
+// Measured on GB300 in graphs: T=7, N=28672, K=4096 NVFP4 19.5 us (3.4 TB/s of
+// weights, half the copy rate: 13.5 us of it are the loop over k, the rest x to
+// f16, sums and the last wave); T=16, N=4096, K=7168 NVFP4 12.8 us, T=32, N=5760,
+// K=2880 MXFP4 14.8 us, T=1, N=2048, K=768 MXFP4 4.0 us (latency: launch, x to
+// f16, one or two chunks per warp, sums, one after the other).
 #include "few_fp4.cuh"
 #include "moe_launch.h"
 #include "rows_common.cuh"

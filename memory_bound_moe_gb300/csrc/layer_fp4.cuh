@@ -1,12 +1,12 @@
 // Kernels of the MoE layer for a few tokens with 4-bit weights, on the inner
 // loop of few_fp4.cuh. See layer_bf16.cu for what fc1 and fc2 compute and how
-// the batch is routed; the activation is f16 here, with exponents of its own, and
-// with NVFP4 already divided by the tensor scale of the expert's w2. Up to 8 tokens the B columns are the tokens themselves;
-// above, they are the expert's own tokens, 8 to a group and two groups to a
-// pass: an expert with more than 16 of at most 32 tokens takes a second pass
-// over its weights (from L2 or not), which is rare enough that two more groups'
-// accumulators in every warp would cost more. (MXFP4, T=8: 117 us in the first
-// form, 151 in the second.)
+// the batch is routed; the activation is f16 with exponents of its own here, and
+// with NVFP4 already divided by the tensor scale of the expert's w2. Up to 8
+// tokens the B columns are the tokens themselves; above, they are the expert's
+// own tokens, 8 to a group and two groups to a pass: an expert with more than 16
+// of at most 32 tokens takes a second pass over its weights (from L2 or not). Two
+// more groups' accumulators in every warp would cost every batch. (MXFP4, T=8:
+// 117 us in the first form, 151 in the second.)
 //   fc1: a tile is 8 gate rows and the same 8 up rows, so 8 columns of one
 //        expert's activation; a block takes an even share of all tiles, RG at a
 //        time. Up to 8 tokens one converted x serves every expert, and if it
@@ -17,10 +17,11 @@
 //        stays within an expert, and the sums are added to the warp's own
 //        [T][16] in shared memory behind it.
 //
-// Measured on GB300 in graphs: MXFP4, T=8, E=32, k=4, H=I=2880 117 us (fc1 70,
-// fc2 45; the bytes take 41.5), NVFP4, T=32, E=8, k=2, H=4096, I=14336 250 us
-// (fc1 143, fc2 112; 119). DRAM 25% to 47% and issue 35% to 53% busy: the
-// conversion's instructions bound both, more than the loads.
+// Measured on GB300 in graphs: MXFP4, T=8, E=32, k=4, H=I=2880 118 us (fc1 three
+// fifths of it; the bytes take 41.5), NVFP4, T=32, E=8, k=2, H=4096, I=14336 252
+// us (fc1 as much; 119). Bound by latency: DRAM is 25% to 47% busy, issue 35%
+// to 53%, no pipe above 36%, with 3 or 4 warps per scheduler whose registers
+// hold all the bytes in flight.
 #pragma once
 
 #include "few_fp4.cuh"
@@ -101,14 +102,10 @@ __global__ void __launch_bounds__(Fp4Block<F, NG>::kMaxThreads, 1) fc1_fp4_kerne
                 }
                 float v = s.row_w[to] * (silu(gate) * up);
                 if constexpr (F == kWNvfp4) v /= g2;   // fc2 sums over experts of different scales
-                // as f16 times a power of two of the token's 8 columns, which lie in 8 neighbouring lanes
-                float most = fabsf(v);
-#pragma unroll
-                for (int i = 1; i < 8; i <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffu << (lane & 24), most, i));
-                const uint32_t ex = most > 0.0f ? min(max(__float_as_uint(most) >> 23, 15u), 254u) : 0u;
                 const uint64_t at = uint64_t(to) * I + j0;
-                a.act[at + o % 8] = f16_bits(ex > 0u ? v * __uint_as_float((268u - ex) << 23) : v);
-                if (o % 8 == 0) a.act_exps[at / 8] = uint8_t(ex);
+                uint32_t exponent;
+                a.act[at + o % 8] = act_to_f16(v, exponent);   // a token's 8 columns: 8 lanes, all here or none
+                if (o % 8 == 0) a.act_exps[at / 8] = uint8_t(exponent);
             }
         }
     }

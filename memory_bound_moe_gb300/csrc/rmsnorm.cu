@@ -14,7 +14,10 @@
 // bytes per thread), add, reduce the sum of squares by shuffles and one
 // shared-memory exchange, scale and store. Rows of more than kMaxWarps * 32 *
 // 4 vectors take the two-pass form, which reads x and the residual again
-// (from L2) for the second half of the work.
+// (from L2) for the second half of the work. The largest one-pass form (four
+// 32-byte vectors a thread, 64 registers: H above 32768) spills about 300 bytes a
+// thread and is still the faster one: T=512, H=65536 58.5 us, MXFP8 55.5, where
+// two passes over 16-byte vectors take 65.8 and 62.4.
 //
 // Bound by bytes: 8 per value (6 + 1 1/32 with MXFP8 alone). Measured on GB300
 // in graphs: T=8192, H=4096 40.4 us, 6.65 TB/s (99% of a copy); with MXFP8 and
