@@ -483,6 +483,159 @@ moe_status_t moe_layer_fp4(const float* logits, int64_t T, int E, int k, int ren
                            const float* w2_global, moe_bf16_t* out, int32_t* topk_ids, float* topk_weights,
                            void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/*
+ * Key-value cache in pages, for the attention of a decode step: the entry
+ * points from here on build a step's block table, fill the cache and attend
+ * over it. The pages that the other entry points cite have no counterpart.
+ *
+ * A cache holds num_pages pages of page_size tokens, each token with a key and
+ * a value of head_dim elements per head. Element (page, token, head, d) of the
+ * keys is k[page * k_page_stride + token * k_token_stride + head * k_head_stride
+ * + d]; the values likewise. Any non-negative strides (in elements) that are
+ * whole 16-byte vectors will do, so pages may hold tokens of all heads or heads
+ * of all tokens, and k and v may be interleaved views of one array. Elements
+ * are bfloat16 (MOE_KV_BF16) or E4M3 bytes (MOE_KV_E4M3) that stand for E4M3 *
+ * k_scale or E4M3 * v_scale. The struct is read during the call; k and v are
+ * device pointers, 16-byte aligned (MOE_ERR_MISALIGNED).
+ * head_dim 64, 128 or 256, page_size a power of two up to MOE_KV_MAX_PAGE_SIZE
+ * (MOE_ERR_UNSUPPORTED); scales between 2^-126 and 2^126, 1 for bfloat16
+ * (MOE_ERR_INVALID_ARG).
+ */
+#define MOE_KV_BF16 0
+#define MOE_KV_E4M3 1
+#define MOE_KV_MAX_PAGE_SIZE 1024
+typedef struct {
+    void* k;
+    void* v;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t num_heads;
+    int32_t head_dim;
+    int32_t type;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    float k_scale, v_scale;
+} moe_kv_cache_t;
+
+/*
+ * Block tables and slot maps of one step, built on the GPU from the requests'
+ * lengths. Request b has c_b = cached[b] tokens in the cache and brings a_b =
+ * added[b] (negative entries count as 0).
+ *
+ *   have_b = ceil(c_b / page_size), need_b = ceil((c_b + a_b) / page_size)
+ *   starts[b] = sum_{b' < b} a_b', starts[B] = their sum (at most 2^31 - 1)
+ *   A request is refused if need_b > max_pages, if its tokens end behind
+ *   max_tokens (starts[b] + a_b > max_tokens), or if pages run out: with n_b =
+ *   need_b - have_b (0 if one of the first two holds), if n_b > 0 and
+ *   sum_{b' <= b} n_b' > *free_count.
+ *   lengths[b] = c_b + a_b (refused: c_b)
+ *   The step takes pages off the top of the stack free_pages[0 .. *free_count):
+ *   its j-th new page is free_pages[*free_count - 1 - j], in the order of the
+ *   requests and of a request's pages. They are written to block_table[b,
+ *   have_b .. need_b); the other entries keep their values.
+ *   *free_count_out = *free_count - the pages taken
+ *   *refused = the number of refused requests
+ *   For token i of starts[b] <= i < starts[b + 1], of a request that was not
+ *   refused: positions[i] = c_b + i - starts[b], slots[i] = block_table[b,
+ *   positions[i] / page_size] * page_size + positions[i] % page_size.
+ *   Every other token i < max_tokens (of a refused request, or behind the last
+ *   request): positions[i] = 0, slots[i] = -1.
+ *
+ * cached, added, lengths [B], starts [B + 1], free_pages [free_capacity],
+ * block_table [B, max_pages], positions [max_tokens]: int32; slots
+ * [max_tokens]: int64; free_count, free_count_out, refused: one int32.
+ * lengths may be cached itself, free_count_out free_count itself (in place),
+ * and refused may be NULL. *free_count outside [0, free_capacity] counts as
+ * the nearer of the two. Entries that block_table already holds are taken as
+ * they are (slots of a negative one are -1); they are read only where a
+ * request's new tokens begin inside a page. Limits: B <= MOE_MAX_REQUESTS,
+ * max_pages * page_size <= 2^30, max_tokens < 2^31 (MOE_ERR_UNSUPPORTED).
+ * B = 0 and max_tokens = 0 are valid. One launch, no workspace.
+ *
+ * moe_page_release gives the pages of finished requests back: for every b
+ * with finished[b] != 0, in order, it pushes block_table[b, 0 ..
+ * ceil(lengths[b] / page_size)) onto free_pages and sets lengths[b] = 0;
+ * *free_count grows by the pages pushed. (The row's entries stay as they are.)
+ * Pages that would pass free_capacity are dropped. All three in place.
+ */
+#define MOE_MAX_REQUESTS 16384
+moe_status_t moe_page_table(const int32_t* cached, const int32_t* added, int64_t B, int page_size, int max_pages,
+                            int64_t max_tokens, const int32_t* free_pages, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* block_table, int32_t* lengths, int32_t* starts,
+                            int32_t* positions, int64_t* slots, int32_t* free_count_out, int32_t* refused,
+                            moe_stream_t stream);
+moe_status_t moe_page_release(const int32_t* finished, int64_t B, int page_size, int max_pages,
+                              const int32_t* block_table, int32_t* lengths, int32_t* free_pages,
+                              int64_t free_capacity, int32_t* free_count, moe_stream_t stream);
+
+/*
+ * Rotary embedding of q and k, and the write of k and v into the cache.
+ *
+ *   With c_i = cos_sin[positions[t], i], s_i = cos_sin[positions[t], rot/2 + i]
+ *   and the pair (a, b) = (x[i], x[rot/2 + i]), or (x[2i], x[2i + 1]) if
+ *   interleaved != 0, i < rot/2:  (a, b) -> (a c_i - b s_i, b c_i + a s_i)
+ *   in float32; columns rot .. head_dim - 1 stay.
+ *   q_out[t] = bf16_rn(rotated q[t]); k_out[t] = bf16_rn(rotated k[t])
+ *   cache keys at slots[t] = bf16_rn(rotated k[t]), or E4M3(rotated k[t] *
+ *   fl(1 / k_scale)); cache values = v[t], or E4M3(v[t] * fl(1 / v_scale)).
+ *   E4M3 is one rounding of the float32 value to nearest even, saturated to
+ *   +-448 (NaN stays NaN). Slot s is token s % page_size of page s / page_size.
+ *
+ * Tokens whose slot lies outside [0, num_pages * page_size), or with a
+ * position outside [0, max_positions), are left out: their rows of q_out and
+ * k_out and the cache keep what they held. Slots of the other tokens must
+ * differ (of two equal ones either is stored, element by element).
+ * q, q_out [N, num_q_heads, head_dim], k, k_out, v [N, num_heads, head_dim]:
+ * bfloat16, 16-byte aligned, the rows of a token dense and tokens `*_stride`
+ * elements apart (a multiple of 8: MOE_ERR_MISALIGNED; at least a token's
+ * row), so that they can be slices of one projection. q_out may be q and k_out
+ * k, with the same stride (in place). num_q_heads may be 0 (q and q_out NULL);
+ * k_out may be NULL. positions [N] int32, slots [N] int64, cos_sin
+ * [max_positions, rot] float32 (16-byte aligned); rot a multiple of 16 up to
+ * head_dim, or 0 (cos_sin may then be NULL and positions are not read).
+ */
+moe_status_t moe_kv_append(const moe_bf16_t* q, int64_t q_stride, const moe_bf16_t* k, int64_t k_stride,
+                           const moe_bf16_t* v, int64_t v_stride, int64_t N, int num_q_heads,
+                           const int32_t* positions, const int64_t* slots, const float* cos_sin,
+                           int64_t max_positions, int rot, int interleaved, const moe_kv_cache_t* cache,
+                           moe_bf16_t* q_out, int64_t q_out_stride, moe_bf16_t* k_out, int64_t k_out_stride,
+                           moe_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache.
+ *
+ *   n_b = lengths[b] within [0, max_pages * page_size]
+ *   J_b = the tokens j < n_b, with window > 0 only j >= n_b - window, whose
+ *         page block_table[b, j / page_size] lies in [0, num_pages)
+ *   x_j = scale * q[b, h] . key(j),  key and value of head h / (num_q_heads / num_heads)
+ *   out[b, h] = bf16_rn( sum_j exp(x_j - m) value(j) / sum_j exp(x_j - m) ),  m = max x_j
+ *   lse[b, h] = m + ln sum_j exp(x_j - m)
+ * An empty J_b, or scores of -infinity alone, give out = 0 and lse = -infinity;
+ * other scores that are not finite make their row's results NaN. The new token's own key is
+ * seen if lengths counts it (as after moe_page_table and moe_kv_append).
+ * Scores, the softmax and all sums are float32. With a bfloat16 cache the
+ * weights exp(..) enter the products as two bfloat16 terms (16 bits); with an
+ * E4M3 cache as f16 (11 bits), and q as f16 times a power of two per row
+ * (exact down to 2^-31 of the row's largest).
+ *
+ * q [B, num_q_heads, head_dim] with tokens q_stride elements apart (as above),
+ * out [B, num_q_heads, head_dim] dense, bfloat16, 16-byte aligned; lse [B,
+ * num_q_heads] float32, may be NULL; block_table [B, max_pages], lengths [B]
+ * int32. num_q_heads a multiple of num_heads; scale finite. Entries of
+ * block_table behind the tokens attended over are not read. Limits: B <
+ * 2^24, num_q_heads <= 1024, max_pages * page_size <= 2^30 (MOE_ERR_UNSUPPORTED).
+ * Results do not depend on timing. workspace: at least
+ * moe_paged_attention_workspace_size(B, num_q_heads, num_heads, head_dim) bytes,
+ * 16-byte aligned; contents need no preparation. Calls that share one must be
+ * ordered, and so must graphs that captured it.
+ */
+moe_status_t moe_paged_attention_workspace_size(int64_t B, int num_q_heads, int num_heads, int head_dim,
+                                                size_t* bytes);
+moe_status_t moe_paged_attention(const moe_bf16_t* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                 const moe_kv_cache_t* cache, const int32_t* block_table, int max_pages,
+                                 const int32_t* lengths, int window, float scale, moe_bf16_t* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -98,6 +98,19 @@ def load_library():
         lib.moe_layer_fp4.argtypes = [_vp, _i64, _int, _int, _int, _vp, _int, _int, _int, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         lib.moe_layer_fp4.restype = _int
+        lib.moe_page_table.argtypes = [_vp, _vp, _i64, _int, _int, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _vp]
+        lib.moe_page_table.restype = _int
+        lib.moe_page_release.argtypes = [_vp, _i64, _int, _int, _vp, _vp, _vp, _i64, _vp, _vp]
+        lib.moe_page_release.restype = _int
+        lib.moe_kv_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _int, _int, _vp, _vp,
+                                      _i64, _vp, _i64, _vp]
+        lib.moe_kv_append.restype = _int
+        lib.moe_paged_attention_workspace_size.argtypes = [_i64, _int, _int, _int, ctypes.POINTER(ctypes.c_size_t)]
+        lib.moe_paged_attention_workspace_size.restype = _int
+        lib.moe_paged_attention.argtypes = [_vp, _i64, _i64, _int, _vp, _vp, _int, _vp, _int, ctypes.c_float, _vp, _vp, _vp,
+                                            ctypes.c_size_t, _vp]
+        lib.moe_paged_attention.restype = _int
         lib.moe_expand.argtypes = [_vp, _i64, _int, _int, _vp, _vp, _vp]
         lib.moe_expand.restype = _int
         lib.moe_swiglu.argtypes = [_vp, _i64, _int, _vp, _vp]
@@ -759,4 +772,212 @@ def moe_layer_fp4(logits: torch.Tensor, x: torch.Tensor, w13_codes: torch.Tensor
         _raw_stream(stream, dev))
     if st:
         raise MoeError("moe_layer_fp4", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Paged key-value cache: block tables, the cache's writes, attention
+# ---------------------------------------------------------------------------
+
+_i64t = torch.int64
+
+
+class _CacheStruct(ctypes.Structure):   # moe_kv_cache_t
+    _fields_ = ([("k", _vp), ("v", _vp), ("num_pages", _i64)]
+                + [(n, ctypes.c_int32) for n in ("page_size", "num_heads", "head_dim", "type")]
+                + [(f"{side}_{n}_stride", _i64) for side in "kv" for n in ("page", "token", "head")]
+                + [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)])
+
+
+class KVCache:
+    """A paged key-value cache: ``k`` and ``v`` [pages, page_size, heads,
+    head_dim], bfloat16, or float8_e4m3fn that stands for E4M3 times
+    ``k_scale`` / ``v_scale``. Any strides with dense heads' rows will do (a
+    transposed view of [pages, heads, page_size, head_dim], views of one array
+    that holds both). The tensors are checked here, once, and kept: the calls
+    that take the cache read and write them."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or t.dtype != k.dtype:
+                raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn for both")
+            if t.dim() != 4 or t.shape != k.shape:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [pages, page_size, heads, head_dim] for both")
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError("k and v must be CUDA tensors of one device")
+            if t.stride(3) != 1:
+                raise ValueError(f"{name}: a head's row must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
+        self.num_pages, self.page_size, self.heads, self.head_dim = k.shape
+        self.device_index = k.get_device()
+        # the stride of an axis of one entry says nothing
+        strides = [s if n > 1 else 0 for t in (k, v) for s, n in zip(t.stride()[:3], t.shape[:3])]
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, int(k.dtype == torch.float8_e4m3fn), *strides,
+                                    self.k_scale, self.v_scale)
+        self._ptr = ctypes.addressof(self._struct)
+
+    def _on(self, dev: int) -> int:
+        if self.device_index != dev:
+            raise ValueError(f"the cache is on cuda:{self.device_index}, expected cuda:{dev}")
+        return self._ptr
+
+
+class PageTable(NamedTuple):
+    lengths: torch.Tensor      # [B] int32, tokens in the cache once the step's are written
+    starts: torch.Tensor       # [B + 1] int32, a request's first token in the step
+    positions: torch.Tensor    # [max_tokens] int32
+    slots: torch.Tensor        # [max_tokens] int64, page * page_size + row; -1: no token
+    free_count: torch.Tensor   # [1] int32
+    refused: torch.Tensor      # [1] int32, requests that got no pages
+
+
+def moe_page_table(cached: torch.Tensor, added: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                   free_count: torch.Tensor, page_size: int, max_tokens: int, *, out: Optional[PageTable] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> PageTable:
+    """One step's block table and slot map: ``cached`` and ``added`` [B]
+    (int32) tokens per request; new pages come off the top of the stack
+    ``free_pages[:free_count]`` (int32, ``free_count`` [1]) and are written to
+    ``block_table [B, max_pages]`` (int32, in place). ``free_count`` is
+    lowered in place unless ``out`` brings another tensor for it; ``out.lengths``
+    may be ``cached`` itself."""
+    if cached.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("cached must be [B], block_table [B, max_pages] and free_pages one-dimensional")
+    B, N = cached.shape[0], int(max_tokens)
+    max_pages = block_table.shape[1]
+    if N < 0:
+        raise ValueError("max_tokens must not be negative")
+    dev = _device(block_table)
+    if out is None:
+        out = PageTable(_new((B,), _i32, block_table, stream), _new((B + 1,), _i32, block_table, stream),
+                        _new((N,), _i32, block_table, stream), _new((N,), _i64t, block_table, stream), free_count,
+                        _new((1,), _i32, block_table, stream))
+    lengths, starts, positions, slots, count_out, refused = out
+    st = _lib_fast().moe_page_table(
+        _addr(cached, "cached", _i32, (B,), dev), _addr(added, "added", _i32, (B,), dev), B, page_size, max_pages, N,
+        _addr(free_pages, "free_pages", _i32, (free_pages.shape[0],), dev), free_pages.shape[0],
+        _addr(free_count, "free_count", _i32, (1,), dev), _addr(block_table, "block_table", _i32, (B, max_pages), dev),
+        _addr(lengths, "lengths", _i32, (B,), dev), _addr(starts, "starts", _i32, (B + 1,), dev),
+        _addr(positions, "positions", _i32, (N,), dev), _addr(slots, "slots", _i64t, (N,), dev),
+        _addr(count_out, "free_count", _i32, (1,), dev), _opt(refused, "refused", _i32, (1,), dev), _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_page_table", st)
+    return out
+
+
+def moe_page_release(finished: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, free_pages: torch.Tensor,
+                     free_count: torch.Tensor, page_size: int, *, stream: Optional[torch.cuda.Stream] = None):
+    """Pushes the pages of the requests with ``finished[b] != 0`` (int32 [B])
+    onto ``free_pages`` and sets their ``lengths`` to 0; ``lengths``,
+    ``free_pages`` and ``free_count`` are updated in place."""
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_pages one-dimensional")
+    B, max_pages = block_table.shape
+    dev = _device(block_table)
+    st = _lib_fast().moe_page_release(
+        _addr(finished, "finished", _i32, (B,), dev), B, page_size, max_pages,
+        _addr(block_table, "block_table", _i32, (B, max_pages), dev), _addr(lengths, "lengths", _i32, (B,), dev),
+        _addr(free_pages, "free_pages", _i32, (free_pages.shape[0],), dev), free_pages.shape[0],
+        _addr(free_count, "free_count", _i32, (1,), dev), _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_page_release", st)
+
+
+def _token_rows(t: torch.Tensor, name: str, shape: tuple, dev: int):
+    """Address and token stride of bfloat16 ``t [N, heads, D]``: the heads of a
+    token dense, tokens any distance apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not _bf16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    n, heads, D = shape
+    step, by_head, by_col = t.stride()
+    if by_col != 1 or (heads > 1 and by_head != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), step if n > 1 else heads * D
+
+
+def moe_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                  slots: torch.Tensor, cos_sin: Optional[torch.Tensor], cache: KVCache, *, interleaved: bool = False,
+                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Rotary embedding of ``q [N, num_q_heads, head_dim]`` and ``k [N, heads,
+    head_dim]`` by ``cos_sin [max_positions, rot]`` (float32, cosines then
+    sines; None: no rotation) at ``positions`` (int32 [N]), and the write of
+    k and ``v`` into ``cache`` at ``slots`` (int64 [N]; a token with a slot
+    outside the cache is left out, its rows of ``q_out`` and ``k_out`` too). q,
+    k and v (bfloat16) may be slices of one projection. Returns ``q_out`` (new
+    when omitted; q itself for in place); the rotated k goes to ``k_out`` too
+    when one is given. ``q`` may be None."""
+    if k.dim() != 3 or (q is not None and q.dim() != 3) or (cos_sin is not None and cos_sin.dim() != 2):
+        raise ValueError("q must be [N, num_q_heads, head_dim], k [N, heads, head_dim] and cos_sin [max_positions, rot]")
+    N = k.shape[0]
+    dev = _device(k)
+    ref = cache._on(dev)
+    shape = (N, cache.heads, cache.head_dim)
+    kp, ks = _token_rows(k, "k", shape, dev)
+    vp, vs = _token_rows(v, "v", shape, dev)
+    qp = qs = op = os_ = nq = 0
+    if q is not None:
+        nq = q.shape[1]
+        qp, qs = _token_rows(q, "q", (N, nq, cache.head_dim), dev)
+        if q_out is None:
+            q_out = _new((N, nq, cache.head_dim), _bf16, q, stream)
+        op, os_ = (qp, qs) if q_out is q else _token_rows(q_out, "q_out", (N, nq, cache.head_dim), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kop, kos = (0, 0) if k_out is None else (kp, ks) if k_out is k else _token_rows(k_out, "k_out", shape, dev)
+    rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    st = _lib_fast().moe_kv_append(
+        qp, qs, kp, ks, vp, vs, N, nq, 0 if rot == 0 else _addr(positions, "positions", _i32, (N,), dev),
+        _addr(slots, "slots", _i64t, (N,), dev), 0 if rot == 0 else _addr(cos_sin, "cos_sin", _f32, (rows, rot), dev), rows, rot,
+        bool(interleaved), ref, op, os_, kop, kos, _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_kv_append", st)
+    return q_out
+
+
+def moe_paged_attention_workspace_size(B: int, num_q_heads: int, num_heads: int, head_dim: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_paged_attention_workspace_size",
+           load_library().moe_paged_attention_workspace_size(int(B), int(num_q_heads), int(num_heads), int(head_dim),
+                                                             ctypes.byref(out)))
+    return out.value
+
+
+def moe_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lengths: torch.Tensor, *,
+                        scale: Optional[float] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+                        lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of one token per sequence, ``q [B, num_q_heads, head_dim]``
+    (bfloat16), over the first ``lengths[b]`` (int32) cached tokens in the
+    pages ``block_table[b]`` (int32 [B, max_pages]), or the last ``window`` of
+    them. ``scale`` defaults to head_dim^-0.5. Returns ``out`` [B, num_q_heads,
+    head_dim]; ``lse`` (float32 [B, num_q_heads]), when given, gets the
+    logarithms of the softmax sums. ``workspace``: a uint8 tensor of
+    ``moe_paged_attention_workspace_size(B, num_q_heads, heads, head_dim)``
+    bytes (allocated when omitted)."""
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [B, num_q_heads, head_dim] and block_table [B, max_pages]")
+    B, nq, D = q.shape
+    dev = _device(q)
+    ref = cache._on(dev)
+    qp, qs = _token_rows(q, "q", (B, nq, cache.head_dim), dev)
+    if out is None:
+        out = _new((B, nq, D), _bf16, q, stream)
+    if workspace is None:
+        workspace = _new((moe_paged_attention_workspace_size(B, nq, cache.heads, D),), _u8, q, stream)
+    ws_bytes = workspace.numel()
+    st = _lib_fast().moe_paged_attention(
+        qp, qs, B, nq, ref, _addr(block_table, "block_table", _i32, (B, block_table.shape[1]), dev), block_table.shape[1],
+        _addr(lengths, "lengths", _i32, (B,), dev), window, D ** -0.5 if scale is None else scale,
+        _addr(out, "out", _bf16, (B, nq, D), dev), _opt(lse, "lse", _f32, (B, nq), dev),
+        _addr(workspace, "workspace", _u8, (ws_bytes,), dev), ws_bytes, _raw_stream(stream, dev))
+    if st:
+        raise MoeError("moe_paged_attention", st)
     return out

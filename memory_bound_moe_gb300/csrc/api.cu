@@ -8,6 +8,8 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
+#include <utility>
 
 namespace {
 
@@ -689,6 +691,304 @@ moe_status_t moe_layer_fp4(const float* logits, int64_t T, int E, int k, int ren
                      topk_weights, workspace, workspace_bytes, stream,
                      {{w13_codes, n}, {w13_scales, fp4_scales(2 * n, format)}, {w2_codes, n / 2},
                       {w2_scales, fp4_scales(n, format)}, {w13_global, gb}, {w2_global, gb}});
+}
+
+namespace {
+
+bool power_of_two(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
+
+int log2_of(int64_t v) {
+    int s = 0;
+    while ((int64_t(1) << s) < v) ++s;
+    return s;
+}
+
+moe_status_t check_pages(int64_t B, int page_size, int max_pages) {
+    if (B < 0 || page_size < 1 || max_pages < 1) return MOE_ERR_INVALID_ARG;
+    if (!power_of_two(page_size) || page_size > MOE_KV_MAX_PAGE_SIZE) return MOE_ERR_UNSUPPORTED;
+    if (int64_t(max_pages) * page_size > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+bool usable_scale(float s) { return s >= 0x1p-126f && s <= 0x1p126f; }   // so is its reciprocal
+
+// The address range of one side of a cache.
+moe_status_t cache_range(const void* p, int64_t pages, int64_t page, int64_t tokens, int64_t token, int64_t heads,
+                         int64_t head, int64_t row_bytes, int esz, Range* out) {
+    if (page < 0 || token < 0 || head < 0) return MOE_ERR_INVALID_ARG;
+    const int vec = 16 / esz;
+    if (page % vec != 0 || token % vec != 0 || head % vec != 0 || !aligned16(p)) return MOE_ERR_MISALIGNED;
+    uint64_t last = 0;
+    for (const auto& d : {std::pair<int64_t, int64_t>{pages, page}, {tokens, token}, {heads, head}}) {
+        uint64_t step = 0;
+        if (__builtin_mul_overflow(uint64_t(d.first - 1), uint64_t(d.second) * esz, &step) || step >> 56 != 0)
+            return MOE_ERR_UNSUPPORTED;
+        last += step;
+    }
+    *out = {p, last + uint64_t(row_bytes)};
+    return MOE_OK;
+}
+
+// The rules of a cache, its view for the kernels and its two address ranges.
+moe_status_t check_cache(const moe_kv_cache_t* c, moe::CacheView* view, Range* k, Range* v) {
+    if (c == nullptr || c->num_pages < 1 || c->num_heads < 1 || c->page_size < 1) return MOE_ERR_INVALID_ARG;
+    if (c->type != MOE_KV_BF16 && c->type != MOE_KV_E4M3) return MOE_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ERR_UNSUPPORTED;
+    if (!power_of_two(c->page_size) || c->page_size > MOE_KV_MAX_PAGE_SIZE) return MOE_ERR_UNSUPPORTED;
+    if (c->num_pages >= (int64_t(1) << 31) || c->num_heads > 1024) return MOE_ERR_UNSUPPORTED;
+    if (!usable_scale(c->k_scale) || !usable_scale(c->v_scale)) return MOE_ERR_INVALID_ARG;
+    if (c->type == MOE_KV_BF16 && (c->k_scale != 1.0f || c->v_scale != 1.0f)) return MOE_ERR_INVALID_ARG;
+    if (c->k == nullptr || c->v == nullptr) return MOE_ERR_INVALID_ARG;
+    const int esz = c->type == MOE_KV_E4M3 ? 1 : 2;
+    moe_status_t st = cache_range(c->k, c->num_pages, c->k_page_stride, c->page_size, c->k_token_stride, c->num_heads,
+                                  c->k_head_stride, int64_t(c->head_dim) * esz, esz, k);
+    if (st != MOE_OK) return st;
+    st = cache_range(c->v, c->num_pages, c->v_page_stride, c->page_size, c->v_token_stride, c->num_heads,
+                     c->v_head_stride, int64_t(c->head_dim) * esz, esz, v);
+    if (st != MOE_OK) return st;
+    view->k = static_cast<uint8_t*>(c->k);
+    view->v = static_cast<uint8_t*>(c->v);
+    view->k_page = c->k_page_stride * esz;
+    view->k_token = c->k_token_stride * esz;
+    view->k_head = c->k_head_stride * esz;
+    view->v_page = c->v_page_stride * esz;
+    view->v_token = c->v_token_stride * esz;
+    view->v_head = c->v_head_stride * esz;
+    view->num_pages = c->num_pages;
+    view->page_shift = log2_of(c->page_size);
+    view->heads = c->num_heads;
+    view->head_dim = c->head_dim;
+    view->e4m3 = c->type == MOE_KV_E4M3;
+    view->k_scale = c->k_scale;
+    view->v_scale = c->v_scale;
+    return MOE_OK;
+}
+
+// Rows of heads * D bfloat16 values, `stride` elements apart.
+moe_status_t check_strided(const void* p, int64_t n, int64_t heads, int D, int64_t stride, Range* out) {
+    const int64_t row = heads * D;
+    if (p == nullptr || stride < row) return MOE_ERR_INVALID_ARG;
+    if (stride % 8 != 0 || !aligned16(p)) return MOE_ERR_MISALIGNED;
+    if (stride >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    *out = {p, 2 * (uint64_t(n - 1) * uint64_t(stride) + uint64_t(row))};
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_page_table(const int32_t* cached, const int32_t* added, int64_t B, int page_size, int max_pages,
+                            int64_t max_tokens, const int32_t* free_pages, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* block_table, int32_t* lengths, int32_t* starts,
+                            int32_t* positions, int64_t* slots, int32_t* free_count_out, int32_t* refused,
+                            moe_stream_t stream) {
+    const moe_status_t st = check_pages(B, page_size, max_pages);
+    if (st != MOE_OK) return st;
+    if (max_tokens < 0 || free_capacity < 0) return MOE_ERR_INVALID_ARG;
+    if (B > MOE_MAX_REQUESTS || max_tokens >= (int64_t(1) << 31) || free_capacity >= (int64_t(1) << 31))
+        return MOE_ERR_UNSUPPORTED;
+    if ((B > 0 && (cached == nullptr || added == nullptr || block_table == nullptr || lengths == nullptr)) ||
+        (max_tokens > 0 && (positions == nullptr || slots == nullptr)) || (free_capacity > 0 && free_pages == nullptr) ||
+        free_count == nullptr || free_count_out == nullptr || starts == nullptr)
+        return MOE_ERR_INVALID_ARG;
+    for (const void* p : std::initializer_list<const void*>{cached, added, free_pages, free_count, block_table, lengths,
+                                                            starts, positions, free_count_out, refused})
+        if (!aligned4(p)) return MOE_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return MOE_ERR_MISALIGNED;
+    const uint64_t b4 = 4 * uint64_t(B), n = uint64_t(max_tokens);
+    const Range i_c{cached, b4}, i_a{added, b4}, i_p{free_pages, 4 * uint64_t(free_capacity)}, i_f{free_count, 4};
+    const Range o_t{block_table, b4 * uint64_t(max_pages)}, o_l{lengths, b4}, o_s{starts, b4 + 4}, o_p{positions, 4 * n},
+        o_q{slots, 8 * n}, o_f{free_count_out, 4}, o_r{refused, refused != nullptr ? 4u : 0u};
+    if (any_overlap({o_t, o_l, o_s, o_p, o_q, o_f, o_r}, {i_a, i_p}) || any_overlap({o_t, o_s, o_p, o_q, o_r}, {i_c, i_f}) ||
+        overlap(o_l, i_f) || overlap(o_f, i_c) || (lengths != cached && overlap(o_l, i_c)))
+        return MOE_ERR_INVALID_ARG;
+    moe::PageTableArgs a = {};
+    a.cached = cached;
+    a.added = added;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.block_table = block_table;
+    a.lengths = lengths;
+    a.starts = starts;
+    a.positions = positions;
+    a.slots = slots;
+    a.free_count_out = free_count_out;
+    a.refused = refused;
+    a.free_capacity = free_capacity;
+    a.B = int(B);
+    a.page_shift = log2_of(page_size);
+    a.max_pages = max_pages;
+    a.max_tokens = int(max_tokens);
+    return from_cuda(moe::launch_page_table(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_page_release(const int32_t* finished, int64_t B, int page_size, int max_pages,
+                              const int32_t* block_table, int32_t* lengths, int32_t* free_pages,
+                              int64_t free_capacity, int32_t* free_count, moe_stream_t stream) {
+    const moe_status_t st = check_pages(B, page_size, max_pages);
+    if (st != MOE_OK) return st;
+    if (free_capacity < 0) return MOE_ERR_INVALID_ARG;
+    if (B > MOE_MAX_REQUESTS || free_capacity >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (B == 0) return MOE_OK;
+    if (finished == nullptr || block_table == nullptr || lengths == nullptr || free_count == nullptr ||
+        (free_capacity > 0 && free_pages == nullptr))
+        return MOE_ERR_INVALID_ARG;
+    for (const void* p : std::initializer_list<const void*>{finished, block_table, lengths, free_pages, free_count})
+        if (!aligned4(p)) return MOE_ERR_MISALIGNED;
+    const uint64_t b4 = 4 * uint64_t(B);
+    if (any_overlap({{lengths, b4}, {free_pages, 4 * uint64_t(free_capacity)}, {free_count, 4}},
+                    {{finished, b4}, {block_table, b4 * uint64_t(max_pages)}}))
+        return MOE_ERR_INVALID_ARG;
+    moe::PageReleaseArgs a = {};
+    a.finished = finished;
+    a.block_table = block_table;
+    a.lengths = lengths;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.free_capacity = free_capacity;
+    a.B = int(B);
+    a.page_shift = log2_of(page_size);
+    a.max_pages = max_pages;
+    return from_cuda(moe::launch_page_release(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_kv_append(const moe_bf16_t* q, int64_t q_stride, const moe_bf16_t* k, int64_t k_stride,
+                           const moe_bf16_t* v, int64_t v_stride, int64_t N, int num_q_heads,
+                           const int32_t* positions, const int64_t* slots, const float* cos_sin,
+                           int64_t max_positions, int rot, int interleaved, const moe_kv_cache_t* cache,
+                           moe_bf16_t* q_out, int64_t q_out_stride, moe_bf16_t* k_out, int64_t k_out_stride,
+                           moe_stream_t stream) {
+    moe::AppendArgs a = {};
+    Range ck, cv;
+    moe_status_t st = check_cache(cache, &a.cache, &ck, &cv);
+    if (st != MOE_OK) return st;
+    const int D = cache->head_dim;
+    if (N < 0 || num_q_heads < 0 || rot < 0 || rot > D || max_positions < 0 || (rot > 0 && max_positions < 1))
+        return MOE_ERR_INVALID_ARG;
+    if (rot % 16 != 0) return MOE_ERR_MISALIGNED;
+    if (N >= (int64_t(1) << 31) || num_q_heads > 1024 || max_positions > (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (N == 0) return MOE_OK;
+    if (slots == nullptr || (rot > 0 && (positions == nullptr || cos_sin == nullptr))) return MOE_ERR_INVALID_ARG;
+    Range i_q{nullptr, 0}, i_k, i_v, o_q{nullptr, 0}, o_k{nullptr, 0};
+    if (num_q_heads > 0) {
+        if ((st = check_strided(q, N, num_q_heads, D, q_stride, &i_q)) != MOE_OK) return st;
+        if ((st = check_strided(q_out, N, num_q_heads, D, q_out_stride, &o_q)) != MOE_OK) return st;
+    }
+    if ((st = check_strided(k, N, cache->num_heads, D, k_stride, &i_k)) != MOE_OK) return st;
+    if ((st = check_strided(v, N, cache->num_heads, D, v_stride, &i_v)) != MOE_OK) return st;
+    if (k_out != nullptr && (st = check_strided(k_out, N, cache->num_heads, D, k_out_stride, &o_k)) != MOE_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0 || (rot > 0 && (!aligned4(positions) || !aligned16(cos_sin))))
+        return MOE_ERR_MISALIGNED;
+    const Range i_s{slots, 8 * uint64_t(N)}, i_p{positions, rot > 0 ? 4 * uint64_t(N) : 0},
+        i_c{cos_sin, 4 * uint64_t(max_positions) * uint64_t(rot)};
+    // Slices of one array interleave: row by row, an output may lie beside an
+    // input, so only arrays with the same stride can be told apart by their rows.
+    const auto apart = [](Range x, int64_t xs, int xh, Range y, int64_t ys, int yh, int D) {
+        if (!overlap(x, y)) return true;
+        if (xs != ys) return false;
+        const int64_t d = (reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p)) / 2;
+        const int64_t at = ((d % xs) + xs) % xs;   // y's row begins here inside x's stride
+        return at >= int64_t(xh) * D && at + int64_t(yh) * D <= xs;
+    };
+    const int kh = cache->num_heads;
+    const bool q_in_place = q_out == q && q_out_stride == q_stride, k_in_place = k_out == k && k_out_stride == k_stride;
+    if (num_q_heads > 0 &&
+        ((!q_in_place && !apart(o_q, q_out_stride, num_q_heads, i_q, q_stride, num_q_heads, D)) ||
+         !apart(o_q, q_out_stride, num_q_heads, i_k, k_stride, kh, D) ||
+         !apart(o_q, q_out_stride, num_q_heads, i_v, v_stride, kh, D)))
+        return MOE_ERR_INVALID_ARG;
+    if (k_out != nullptr &&
+        ((!k_in_place && !apart(o_k, k_out_stride, kh, i_k, k_stride, kh, D)) ||
+         (num_q_heads > 0 && (!apart(o_k, k_out_stride, kh, i_q, q_stride, num_q_heads, D) ||
+                              !apart(o_k, k_out_stride, kh, o_q, q_out_stride, num_q_heads, D))) ||
+         !apart(o_k, k_out_stride, kh, i_v, v_stride, kh, D)))
+        return MOE_ERR_INVALID_ARG;
+    for (const Range& c : {ck, cv})
+        for (const Range& r : {i_q, i_k, i_v, o_q, o_k, i_s, i_p, i_c})
+            if (overlap(c, r)) return MOE_ERR_INVALID_ARG;
+    for (const Range& o : {o_q, o_k})
+        for (const Range& r : {i_s, i_p, i_c})
+            if (overlap(o, r)) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if (current_sm_count(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.positions = positions;
+    a.slots = slots;
+    a.cos_sin = cos_sin;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.max_positions = max_positions;
+    a.N = int(N);
+    a.q_heads = num_q_heads;
+    a.rot = rot;
+    a.interleaved = interleaved != 0;
+    return from_cuda(moe::launch_kv_append(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+moe_status_t check_attention_sizes(int64_t B, int num_q_heads, int num_heads, int head_dim) {
+    if (B < 0 || num_q_heads < 1 || num_heads < 1 || num_q_heads % num_heads != 0) return MOE_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return MOE_ERR_UNSUPPORTED;
+    if (B >= (int64_t(1) << 24) || num_q_heads > 1024) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_paged_attention_workspace_size(int64_t B, int num_q_heads, int num_heads, int head_dim,
+                                                size_t* bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    const moe_status_t st = check_attention_sizes(B, num_q_heads, num_heads, head_dim);
+    if (st != MOE_OK) return st;
+    *bytes = B == 0 ? 0 : moe::paged_attention_workspace(B, num_q_heads, num_heads, head_dim);
+    return MOE_OK;
+}
+
+moe_status_t moe_paged_attention(const moe_bf16_t* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                 const moe_kv_cache_t* cache, const int32_t* block_table, int max_pages,
+                                 const int32_t* lengths, int window, float scale, moe_bf16_t* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    moe::AttentionArgs a = {};
+    Range ck, cv, i_q;
+    moe_status_t st = check_cache(cache, &a.cache, &ck, &cv);
+    if (st != MOE_OK) return st;
+    if ((st = check_attention_sizes(B, num_q_heads, cache->num_heads, cache->head_dim)) != MOE_OK) return st;
+    if ((st = check_pages(B, cache->page_size, max_pages)) != MOE_OK) return st;
+    if (window < 0 || !(scale >= -3.402823466e38f && scale <= 3.402823466e38f)) return MOE_ERR_INVALID_ARG;
+    if (B == 0) return MOE_OK;
+    const int D = cache->head_dim;
+    if ((st = check_strided(q, B, num_q_heads, D, q_stride, &i_q)) != MOE_OK) return st;
+    if (block_table == nullptr || lengths == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(lengths) || !aligned16(out) || !aligned4(lse)) return MOE_ERR_MISALIGNED;
+    const uint64_t need = moe::paged_attention_workspace(B, num_q_heads, cache->num_heads, D);
+    if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOE_ERR_MISALIGNED;
+    const uint64_t heads = uint64_t(B) * uint64_t(num_q_heads);
+    if (any_overlap({{out, 2 * heads * D}, {lse, lse != nullptr ? 4 * heads : 0}, {workspace, need}},
+                    {i_q, ck, cv, {block_table, 4 * uint64_t(B) * uint64_t(max_pages)}, {lengths, 4 * uint64_t(B)}}))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if (current_sm_count(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+    a.q = q;
+    a.block_table = block_table;
+    a.lengths = lengths;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.q_stride = q_stride;
+    a.B = int(B);
+    a.q_heads = num_q_heads;
+    a.max_pages = max_pages;
+    a.window = window;
+    a.scale = scale;
+    return from_cuda(moe::launch_paged_attention(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

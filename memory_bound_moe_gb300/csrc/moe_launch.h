@@ -117,4 +117,79 @@ cudaError_t launch_layer_bf16(const LayerArgs& a, int num_sms, cudaStream_t stre
 cudaError_t launch_layer_nvfp4(const LayerArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_layer_mxfp4(const LayerArgs& a, int num_sms, cudaStream_t stream);
 
+// Block tables and slot maps (page_table.cu). Sums over the requests are 64-bit.
+constexpr int kMaxRequests = 16384;   // MOE_MAX_REQUESTS
+struct PageTableArgs {
+    const int32_t* cached;       // may be lengths
+    const int32_t* added;
+    const int32_t* free_pages;
+    const int32_t* free_count;   // may be free_count_out
+    int32_t* block_table;
+    int32_t* lengths;
+    int32_t* starts;
+    int32_t* positions;
+    int64_t* slots;
+    int32_t* free_count_out;
+    int32_t* refused;            // may be NULL
+    int64_t free_capacity;
+    int B, page_shift, max_pages, max_tokens;
+};
+cudaError_t launch_page_table(const PageTableArgs& a, cudaStream_t stream);
+struct PageReleaseArgs {
+    const int32_t* finished;
+    const int32_t* block_table;
+    int32_t* lengths;
+    int32_t* free_pages;
+    int32_t* free_count;
+    int64_t free_capacity;
+    int B, page_shift, max_pages;
+};
+cudaError_t launch_page_release(const PageReleaseArgs& a, cudaStream_t stream);
+
+// A paged key-value cache as the kernels see it: strides in bytes.
+struct CacheView {
+    uint8_t* k;
+    uint8_t* v;
+    int64_t k_page, k_token, k_head;
+    int64_t v_page, v_token, v_head;
+    int64_t num_pages;
+    int page_shift, heads, head_dim;
+    bool e4m3;
+    float k_scale, v_scale;
+};
+
+// Rotary embedding and the cache's writes (kv_append.cu).
+struct AppendArgs {
+    CacheView cache;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* q_out;
+    uint16_t* k_out;             // may be NULL
+    const int32_t* positions;
+    const int64_t* slots;
+    const float* cos_sin;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   // elements
+    int64_t max_positions;
+    int N, q_heads, rot;
+    bool interleaved;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, int num_sms, cudaStream_t stream);
+
+// Attention of one token per sequence over the cache (paged_attention.cu).
+struct AttentionArgs {
+    CacheView cache;
+    const uint16_t* q;
+    const int32_t* block_table;
+    const int32_t* lengths;
+    uint16_t* out;
+    float* lse;                  // may be NULL
+    void* workspace;
+    int64_t q_stride;            // elements
+    int B, q_heads, max_pages, window;
+    float scale;
+};
+size_t paged_attention_workspace(int64_t B, int q_heads, int heads, int head_dim);
+cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream);
+
 }  // namespace moe
