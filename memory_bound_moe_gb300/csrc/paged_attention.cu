@@ -7,18 +7,20 @@
 // cache bounds it, and mma.sync keeps up with HBM at a quarter of its rate; a
 // 128-row tcgen05 tile would be empty to seven eighths or more.
 //
-// Split. A unit of work is (sequence, key head, group of 16 heads); its tiles
-// are 64 tokens. All units' tiles, one after another, are cut into equal runs,
-// one per resident block: whatever the lengths are, every SM reads the same
-// number of bytes (the lengths are on the GPU, so every block adds them up for
-// itself). A unit inside one run is finished there; what a run has of a unit
-// that goes on in another run goes to the workspace (at most two per run), and
-// a second kernel joins those in order of the runs.
+// Split. A unit of work is (sequence, key head, group of 16 heads). All units'
+// tiles, one after another, are cut into equal runs, one per resident block:
+// whatever the lengths are, every SM reads the same number of bytes (the
+// lengths are on the GPU, so every block adds them up for itself). A unit
+// inside one run is finished there; what a run has of a unit that goes on in
+// another run goes to the workspace (at most two per run), and a second kernel
+// joins those in order of the runs.
 //
-// A block's 4 warps take 16 tokens of a tile each and never meet inside a unit:
-// each has its own ring of kStages steps in shared memory, filled by 16-byte
-// cp.async, and its own running maximum, sum and output (online softmax); the
-// four are joined when the run leaves the unit.
+// A block's 4 warps take a step (16 or 32 tokens) of a tile each and never meet
+// inside a unit: each has its own ring of kStages steps in shared memory, filled
+// by 16-byte cp.async, and its own running maximum, sum and output (online
+// softmax); the four are joined when the run leaves the unit. The ring goes on
+// over the units: the next ones' first steps are on their way while one is
+// finished, in the stage that was read last.
 #include "few_device.cuh"
 #include "moe_launch.h"
 
@@ -27,12 +29,16 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kNt = kWarps * kWarp;
-constexpr int kRows = 16;            // query heads of a unit
-constexpr int kStep = 16;            // tokens of a warp's step
-constexpr int kTile = kWarps * kStep;
-constexpr int kStages = 3;
+constexpr int kRows = 16;            // query heads of a unit, at most
+#ifndef MOE_ATTN_STAGES
+#define MOE_ATTN_STAGES 3
+#endif
+constexpr int kStages = MOE_ATTN_STAGES;
 constexpr int kMaxBlocks = 640;      // runs the workspace holds the ends of
-constexpr int kMinTiles = 2;         // tiles of a run, at least
+#ifndef MOE_ATTN_MIN_TILES
+#define MOE_ATTN_MIN_TILES 2
+#endif
+constexpr int kMinTiles = MOE_ATTN_MIN_TILES;   // tiles of a run, at least
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // ---------------------------------------------------------------------------
@@ -66,6 +72,10 @@ __host__ __device__ inline Partials partials(void* ws, int blocks, int rows, int
 // ---------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     const int n = valid ? 16 : 0;   // 0: zeros, nothing is read
@@ -118,38 +128,52 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 // The tokens of a sequence, and where a run begins
 // ---------------------------------------------------------------------------
 
+// TILE tokens to a tile, counted from the one that holds `first`.
 struct Span {
-    int first, len, tiles;   // tokens first .. len - 1; tiles counted from first / kTile
-    __device__ __forceinline__ int tile0() const { return first / kTile; }
+    int first, len, tiles;   // tokens first .. len - 1
 };
 
+template <int TILE>
 __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
     Span s;
     const int64_t most = int64_t(a.max_pages) << a.cache.page_shift;
-    s.len = int(min(int64_t(max(a.lengths[b], 0)), most));
+    s.len = int(min(int64_t(max(__ldg(a.lengths + b), 0)), most));
     s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
-    s.tiles = s.len == 0 ? 0 : (s.len - 1) / kTile + 1 - s.tile0();
+    s.tiles = s.len == 0 ? 0 : (s.len - 1) / TILE + 1 - s.first / TILE;
     return s;
 }
 
-struct Place {
-    int64_t run;      // tiles of a run
-    int64_t total;    // tiles of all units
-    int64_t base;     // tiles before sequence b's units
-    int b;            // the sequence in which this block's run begins
+// A place in a run: `left` tiles of it from tile `local` of unit `unit` of
+// sequence b on.
+template <int TILE>
+struct Cursor {
+    int64_t left;
+    int b, unit, local;
+    Span s;
+    __device__ __forceinline__ int tiles() const { return int(min(int64_t(s.tiles - local), left)); }   // of this unit
+    __device__ __forceinline__ void next_unit(const AttentionArgs& a, int units) {
+        left -= tiles();
+        local = 0;
+        if (++unit == units && left > 0) {
+            unit = 0;
+            do s = span_of<TILE>(a, ++b);
+            while (s.tiles == 0);
+        }
+    }
 };
 
-// Every block adds up the sequences' tiles for itself. A thread's sequences
-// are a run of them, so that the thread in whose range this block's run begins
-// can walk to its sequence.
-__device__ __forceinline__ Place find_run(const AttentionArgs& a, int units) {
+// This block's run. Every block adds up the sequences' tiles for itself. A
+// thread's sequences are a run of them, so that the thread in whose range this
+// block's run begins can walk to its sequence. `run`: tiles of a run.
+template <int TILE>
+__device__ __forceinline__ Cursor<TILE> find_run(const AttentionArgs& a, int units, int64_t& run) {
     __shared__ int64_t s_warp[kWarps];
     __shared__ int64_t s_base;
     __shared__ int s_b;
     const int per = (a.B + kNt - 1) / kNt, b0 = min(a.B, int(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     int64_t sum = 0;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) sum += span_of(a, b).tiles;
+    for (int b = b0; b < b1; ++b) sum += span_of<TILE>(a, b).tiles;
     sum *= units;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     int64_t x = sum;
@@ -166,69 +190,101 @@ __device__ __forceinline__ Place find_run(const AttentionArgs& a, int units) {
         if (w < warp) before += s_warp[w];
         total += s_warp[w];
     }
-    Place p;
-    p.total = total;
-    p.run = max(int64_t(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
-    const int64_t start = p.run * blockIdx.x;
+    run = max(int64_t(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
+    const int64_t start = run * blockIdx.x;
     if (before <= start && start < before + sum) {
         int b = b0;
-        int64_t n = int64_t(span_of(a, b).tiles) * units;
+        int64_t n = int64_t(span_of<TILE>(a, b).tiles) * units;
         while (before + n <= start) {
             before += n;
-            n = int64_t(span_of(a, ++b).tiles) * units;
+            n = int64_t(span_of<TILE>(a, ++b).tiles) * units;
         }
         s_base = before;
         s_b = b;
     }
     __syncthreads();
-    p.base = s_base;
-    p.b = s_b;
-    return p;
+    Cursor<TILE> c = {};
+    c.left = max(int64_t(0), min(run, total - start));
+    if (c.left > 0) {
+        c.b = s_b;
+        c.s = span_of<TILE>(a, c.b);
+        c.unit = int((start - s_base) / c.s.tiles);
+        c.local = int((start - s_base) % c.s.tiles);
+    }
+    return c;
 }
 
 // ---------------------------------------------------------------------------
-// Main kernel
+// Main kernel: NH groups of 8 query heads
 // ---------------------------------------------------------------------------
 
 template <int D, bool E4M3>
 struct Tile {
-    static constexpr int kBytes = D * (E4M3 ? 1 : 2);      // of a token's head
+    static constexpr int kStep = E4M3 || D == 64 ? 32 : 16;   // tokens of a warp's step
+    static constexpr int kTile = kWarps * kStep;
+    static constexpr int kBytes = D * (E4M3 ? 1 : 2);         // of a token's head
     static constexpr int kVecs = kBytes / 16;
-    static constexpr int kSide = kStep * kBytes;           // keys or values of a step
-    static constexpr int kRing = kStages * 2 * kSide;      // of a warp
-    static constexpr int kPitch = D + 8;                   // floats between output rows: no bank conflicts
+    static constexpr int kPer = kWarp / kVecs;                // rows that a warp copies with one instruction
+    static constexpr int kSide = kStep * kBytes;              // keys or values of a step
+    static constexpr int kStage = 2 * kSide;
+    static constexpr int kRing = kStages * kStage;            // of a warp
     static constexpr int kSmem = kWarps * kRing;
-    static_assert(kRows * kPitch * 4 <= kRing, "a warp's output takes the place of its ring");
+    static_assert(kRows * D * 4 <= kStage, "a warp's output takes the place of a stage");
     // 16-byte vector v of row r lies at v ^ swz(r): 8 rows at the same vector hit 8 different banks of 16 bytes
     static __device__ __forceinline__ int swz(int r) { return kVecs >= 8 ? r & 7 : (r >> 1) & 3; }
     static __device__ __forceinline__ uint32_t at(int r, int v) { return uint32_t(r * kBytes + ((v ^ swz(r)) << 4)); }
+    // float d of output row r, in a stage
+    static __device__ __forceinline__ int out_at(int r, int d) { return r * D + (d ^ (((r >> 1) & 3) * 8)); }
 };
 
-// One side (keys or values) of a step into shared memory: row r from src + its
-// page's and token's offset.
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+    return (int64_t(__shfl_sync(kFull, int(v >> 32), lane)) << 32) | uint32_t(__shfl_sync(kFull, int(v), lane));
+}
+
+// A step's keys and values into a stage. page: that of token t0 + lane %
+// kStep; mask: the tokens to be read, the others become zeros.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_side(uint32_t dst, const uint8_t* src, int page_shift, int64_t page_stride, int64_t token_stride,
-                                          int page, int t0, uint32_t mask) {
+__device__ __forceinline__ void load_step(uint32_t dst, const CacheView& c, const uint8_t* k, const uint8_t* v, int t0, int page,
+                                          uint32_t mask) {
     using T = Tile<D, E4M3>;
-    constexpr int kPer = kWarp / T::kVecs > 0 ? kWarp / T::kVecs : 1;   // rows per instruction
-    const int lane = threadIdx.x % kWarp, v = lane % T::kVecs;
-    const int in_page = (1 << page_shift) - 1;
+    const int lane = threadIdx.x % kWarp, vec = lane % T::kVecs, row = lane / T::kVecs;
+    const int in_page = (1 << c.page_shift) - 1;
+    constexpr uint32_t kAll = T::kStep == 32 ? 0xffffffffu : 0xffffu;
+    if (mask == kAll && c.page_shift >= 4) {
+        // 16 tokens in a row are one page's
 #pragma unroll
-    for (int i = 0; i < kStep / kPer; ++i) {
-        const int r = i * kPer + lane / T::kVecs;
-        const int pg = page_shift >= 4 ? page : __shfl_sync(kFull, page, r);
+        for (int r0 = 0; r0 < T::kStep; r0 += 16) {
+            const int64_t pg = __shfl_sync(kFull, page, r0);
+            const int t = ((t0 + r0) & in_page) + row;
+            const uint8_t* kp = k + pg * c.k_page + t * c.k_token + vec * 16;
+            const uint8_t* vp = v + pg * c.v_page + t * c.v_token + vec * 16;
+#pragma unroll
+            for (int i = 0; i < 16; i += T::kPer) {
+                cp_async16(dst + T::at(r0 + i + row, vec), kp + i * c.k_token);
+                cp_async16(dst + T::kSide + T::at(r0 + i + row, vec), vp + i * c.v_token);
+            }
+        }
+        return;
+    }
+    const int64_t pg = page, t = (t0 + lane % T::kStep) & in_page;   // this lane's row's, where it is valid
+    const int64_t ko = pg * c.k_page + t * c.k_token, vo = pg * c.v_page + t * c.v_token;
+#pragma unroll
+    for (int i = 0; i < T::kStep; i += T::kPer) {
+        const int r = i + row;
         const bool valid = (mask >> r) & 1u;
-        const uint8_t* p = src + (valid ? int64_t(pg) * page_stride + int64_t((t0 + r) & in_page) * token_stride + v * 16 : 0);
-        cp_async16(dst + T::at(r, v), p, valid);
+        const int64_t kr = shfl64(ko, r), vr = shfl64(vo, r);
+        cp_async16(dst + T::at(r, vec), k + (valid ? kr + vec * 16 : 0), valid);
+        cp_async16(dst + T::kSide + T::at(r, vec), v + (valid ? vr + vec * 16 : 0), valid);
     }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NH>
 __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, int groups) {
     using T = Tile<D, E4M3>;
-    constexpr int kD16 = D / 16;
+    constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ const float* s_out[kWarps];
     pdl_wait_and_release();
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, quad = lane % 4;
     const int heads = a.cache.heads, group = a.q_heads / heads, units = heads * groups;
@@ -238,40 +294,85 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
 
     // sequences without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (span_of(a, b).tiles == 0) {
+        if (span_of<T::kTile>(a, b).tiles == 0) {
             uint4* o = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.q_heads * D);
             for (int i = threadIdx.x; i < a.q_heads * D / 8; i += kNt) o[i] = make_uint4(0, 0, 0, 0);
             if (a.lse != nullptr)
                 for (int i = threadIdx.x; i < a.q_heads; i += kNt) a.lse[int64_t(b) * a.q_heads + i] = -INFINITY;
         }
 
-    const Place place = find_run(a, units);
-    int64_t pos = place.run * blockIdx.x;
-    const int64_t end = min(place.total, pos + place.run);
+    int64_t run = 0;
+    Cursor<T::kTile> c = find_run<T::kTile>(a, units, run);
+    // this warp's steps of a cursor's unit: tokens from + (j kWarps + warp) kStep on
+    const auto open = [&](const Cursor<T::kTile>& p, int& from) {
+        const int begin = (p.s.first / T::kTile + p.local) * T::kTile;
+        from = max(begin, p.s.first & ~(kStep - 1));
+        const int to = min(p.s.len, begin + p.tiles() * T::kTile);
+        return ((to - from + kStep - 1) / kStep - warp + kWarps - 1) / kWarps;
+    };
+
+    // The loads run ahead of the products, over the units' ends: `ahead` is
+    // where they are, next_t0 and next_page the step to be loaded next.
+    Cursor<T::kTile> ahead = c;
+    int ahead_from = 0, ahead_j = 0, ahead_steps = 0, next_t0 = 0, next_page = -1;
+    bool more = c.left > 0;
+    if (more) ahead_steps = open(ahead, ahead_from);
+    const auto look = [&]() {
+        while (more && ahead_j >= ahead_steps) {
+            ahead.next_unit(a, units);
+            more = ahead.left > 0;
+            ahead_j = 0;
+            if (more) ahead_steps = open(ahead, ahead_from);
+        }
+        next_page = -1;
+        if (more) {
+            next_t0 = ahead_from + (ahead_j++ * kWarps + warp) * kStep;
+            const int t = next_t0 + lane % kStep;
+            if (t >= ahead.s.first && t < ahead.s.len) {
+                const int pg = __ldg(a.block_table + int64_t(ahead.b) * a.max_pages + (t >> a.cache.page_shift));
+                next_page = pg < a.cache.num_pages ? pg : -1;
+            }
+        }
+    };
+    const auto issue = [&](int stage) -> uint32_t {
+        uint32_t mask = __ballot_sync(kFull, next_page >= 0);
+        if (kStep == 16) mask &= 0xffffu;
+        if (more) {
+            const int64_t head = ahead.unit / groups;
+            load_step<D, E4M3>(ring_at + stage * T::kStage, a.cache, a.cache.k + head * a.cache.k_head,
+                               a.cache.v + head * a.cache.v_head, next_t0, next_page, mask);
+        }
+        cp_commit();
+        look();
+        return mask;
+    };
+    uint32_t masks[kStages];   // of the steps in the ring, the oldest first
+    look();
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) masks[i] = issue(i);
+    int stage = 0;             // of the step that comes next
+
     Note note = {-1, 0, 0, 0};
-    int b = place.b;
-    Span s = {};
-    int unit = 0, local = 0;
-    if (pos < end) {
-        s = span_of(a, b);
-        unit = int((pos - place.base) / s.tiles);
-        local = int((pos - place.base) % s.tiles);
-    }
-    while (pos < end) {
-        const int seg = int(min(int64_t(s.tiles - local), end - pos));
-        const int head = unit / groups, chunk = unit % groups;
+    int64_t pos = run * blockIdx.x;
+    while (c.left > 0) {
+        const int head = c.unit / groups, chunk = c.unit % groups;
         const int rows = min(kRows, group - chunk * kRows);
         const int h0 = head * group + chunk * kRows;
 
         // q, as A: row g (and g + 8) is head h0 + g. For E4M3 the order of the 16 columns of a
         // product is that in which the keys' bytes come out of ldmatrix: 4 quad .. 4 quad + 3.
         uint32_t aq[kD16][4];
-        float c[2];   // what a row's scores are multiplied by, with log2 e
+        float f_row[NH];   // what a row's scores are multiplied by, with log2 e
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            if (h >= NH) {
+#pragma unroll
+                for (int k = 0; k < kD16; ++k) aq[k][h] = aq[k][h + 2] = 0u;
+                continue;
+            }
             const int r = g + 8 * h;
-            const uint16_t* q = a.q + int64_t(b) * a.q_stride + int64_t(h0 + r) * D;
-            c[h] = a.scale * a.cache.k_scale * kLog2e;
+            const uint16_t* q = a.q + int64_t(c.b) * a.q_stride + int64_t(h0 + r) * D;
+            f_row[h] = a.scale * a.cache.k_scale * kLog2e;
             if constexpr (!E4M3) {
 #pragma unroll
                 for (int k = 0; k < kD16; ++k) {
@@ -279,211 +380,198 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
                     aq[k][h + 2] = r < rows ? *reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2 + 8) : 0u;
                 }
             } else {
-                uint2 w[kD16];
                 float most = 0.0f;
 #pragma unroll
                 for (int k = 0; k < kD16; ++k) {
-                    w[k] = r < rows ? *reinterpret_cast<const uint2*>(q + k * 16 + quad * 4) : make_uint2(0u, 0u);
-                    most = fmaxf(fmaxf(most, fmaxf(fabsf(bf16_lo(w[k].x)), fabsf(bf16_hi(w[k].x)))),
-                                 fmaxf(fabsf(bf16_lo(w[k].y)), fabsf(bf16_hi(w[k].y))));
+                    const uint2 w = r < rows ? *reinterpret_cast<const uint2*>(q + k * 16 + quad * 4) : make_uint2(0u, 0u);
+                    aq[k][h] = w.x;
+                    aq[k][h + 2] = w.y;
+                    most = fmaxf(fmaxf(most, fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x)))),
+                                 fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y))));
                 }
                 most = fmaxf(most, __shfl_xor_sync(kFull, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(kFull, most, 2));
                 // f16 holds q times 2^(14 - e), e the exponent of the row's largest (1 for a row of zeros or with an infinity)
                 const int e = most > 0.0f && most < INFINITY ? max(int(__float_as_uint(most) >> 23) - 127, -112) : 14;
                 const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
-                c[h] *= __uint_as_float(uint32_t(127 - 14 + e) << 23);
+                f_row[h] *= __uint_as_float(uint32_t(127 - 14 + e) << 23);
 #pragma unroll
                 for (int k = 0; k < kD16; ++k) {
-                    aq[k][h] = pack_f16x2(bf16_lo(w[k].x) * up, bf16_hi(w[k].x) * up);
-                    aq[k][h + 2] = pack_f16x2(bf16_lo(w[k].y) * up, bf16_hi(w[k].y) * up);
+                    aq[k][h] = pack_f16x2(bf16_lo(aq[k][h]) * up, bf16_hi(aq[k][h]) * up);
+                    aq[k][h + 2] = pack_f16x2(bf16_lo(aq[k][h + 2]) * up, bf16_hi(aq[k][h + 2]) * up);
                 }
             }
         }
 
-        float o[D / 8][4] = {};
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        {
-            // this warp's steps: tokens t_at(j) .. t_at(j) + 15
-            const int begin = (s.tile0() + local) * kTile;
-            const int from = max(begin, s.first & ~(kStep - 1)), to = min(s.len, begin + seg * kTile);
-            const int steps_all = (to - from + kStep - 1) / kStep;
-            const int steps = (steps_all - warp + kWarps - 1) / kWarps;
-            const auto t_at = [&](int j) { return from + (j * kWarps + warp) * kStep; };
-            const int32_t* table = a.block_table + int64_t(b) * a.max_pages;
-            const uint8_t* kp = a.cache.k + head * a.cache.k_head;
-            const uint8_t* vp = a.cache.v + head * a.cache.v_head;
-            // the page of token t_at(j) + lane % 16; -1 where there is none
-            const auto page_of = [&](int j) {
-                if (j >= steps) return -1;
-                const int t = t_at(j) + lane % kStep;
-                if (t < s.first || t >= s.len) return -1;
-                const int pg = table[t >> a.cache.page_shift];
-                return pg < a.cache.num_pages ? pg : -1;
-            };
-            const auto issue = [&](int j, int page) -> uint32_t {
-                const uint32_t mask = __ballot_sync(kFull, page >= 0) & 0xffffu;
-                if (j < steps) {
-                    const uint32_t dst = ring_at + (j % kStages) * 2 * T::kSide;
-                    int pg = page;
-                    if (a.cache.page_shift >= 4) pg = __shfl_sync(kFull, page, mask != 0 ? __ffs(mask) - 1 : 0);
-                    load_side<D, E4M3>(dst, kp, a.cache.page_shift, a.cache.k_page, a.cache.k_token, pg, t_at(j), mask);
-                    load_side<D, E4M3>(dst + T::kSide, vp, a.cache.page_shift, a.cache.v_page, a.cache.v_token, pg, t_at(j), mask);
-                }
-                cp_commit();
-                return mask;
-            };
-            uint32_t masks[kStages];
-            int pages[kStages];
+        // out^T: [16 columns][8 heads][row g: heads 2 quad, 2 quad + 1; row g + 8: the same]
+        float o[kD16][NH][4];
+        float m[NH], l[NH];
 #pragma unroll
-            for (int i = 0; i < kStages; ++i) pages[i] = page_of(i);
+        for (int h = 0; h < NH; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.0f;
 #pragma unroll
-            for (int i = 0; i + 1 < kStages; ++i) masks[i] = issue(i, pages[i]);
-            int page = pages[kStages - 1];
-            for (int j = 0; j < steps; ++j) {
-                cp_wait<kStages - 2>();
-                __syncwarp();
-                masks[kStages - 1] = issue(j + kStages - 1, page);
-                page = page_of(j + kStages);
-                const uint32_t ks = ring_at + (j % kStages) * 2 * T::kSide, vs = ks + T::kSide;
-                const uint32_t mask = masks[0];
+            for (int d = 0; d < kD16; ++d)
 #pragma unroll
-                for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
+                for (int z = 0; z < 4; ++z) o[d][h][z] = 0.0f;
+        }
+        int from = 0;
+        const int steps = open(c, from);
+        for (int j = 0; j < steps; ++j) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            masks[kStages - 1] = issue(stage == 0 ? kStages - 1 : stage - 1);
+            const uint32_t ks = ring_at + stage * T::kStage, vs = ks + T::kSide;
+            const uint32_t mask = masks[0];
+#pragma unroll
+            for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
+            stage = stage + 1 == kStages ? 0 : stage + 1;
 
-                float x[2][4] = {};   // [8 tokens][row g: tokens 2 quad, 2 quad + 1; row g + 8: the same]
+            float x[kTiles8][4] = {};   // [8 tokens][row g: tokens 2 quad, 2 quad + 1; row g + 8: the same]
+#pragma unroll
+            for (int t = 0; t < kStep; t += 16) {
                 if constexpr (!E4M3) {
-                    const int row = lane % 8 + (lane & 16) / 2, v = (lane >> 3) & 1;
+                    const int row = t + lane % 8 + (lane & 16) / 2, v = (lane >> 3) & 1;
 #pragma unroll
                     for (int k = 0; k < kD16; ++k) {
                         uint32_t r[4];
                         ldsm(r, ks + T::at(row, 2 * k + v));
-                        mma<false>(x[0], aq[k], r[0], r[1]);
-                        mma<false>(x[1], aq[k], r[2], r[3]);
+                        mma<false>(x[t / 8], aq[k], r[0], r[1]);
+                        mma<false>(x[t / 8 + 1], aq[k], r[2], r[3]);
                     }
                 } else {
-                    const int row = lane % 16, v = lane >> 4;
+                    const int row = t + lane % 16, v = lane >> 4;
 #pragma unroll
                     for (int k = 0; k < kD16; k += 2) {
                         uint32_t r[4];
                         ldsm(r, ks + T::at(row, k + v));
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                            mma<true>(x[z & 1], aq[k + z / 2], e4m3x2_to_f16x2(r[z]), e4m3x2_to_f16x2(r[z] >> 16));
+                            mma<true>(x[t / 8 + (z & 1)], aq[k + z / 2], e4m3x2_to_f16x2(r[z]), e4m3x2_to_f16x2(r[z] >> 16));
                     }
                 }
-                float top[2] = {-INFINITY, -INFINITY};
+            }
+            constexpr uint32_t kAll = kStep == 32 ? 0xffffffffu : 0xffffu;
+            float top[NH];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+            for (int h = 0; h < NH; ++h) {
+                top[h] = -INFINITY;
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const bool seen = (mask >> (n * 8 + quad * 2 + (z & 1))) & 1u;
-                        x[n][z] = seen ? x[n][z] * c[z >> 1] : -INFINITY;
-                        top[z >> 1] = fmaxf(top[z >> 1], x[n][z]);
+                for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) x[n][2 * h + z] *= f_row[h];
+            }
+            if (mask != kAll) {
+                const uint32_t seen = mask >> (quad * 2);
+#pragma unroll
+                for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+                    for (int z = 0; z < 2 * NH; ++z)
+                        if (!((seen >> (n * 8 + (z & 1))) & 1u)) x[n][z] = -INFINITY;
+            }
+            bool higher = false;
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+#pragma unroll
+                for (int n = 0; n < kTiles8; ++n) top[h] = fmaxf(top[h], fmaxf(x[n][2 * h], x[n][2 * h + 1]));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+                higher |= top[h] > m[h];
+            }
+            if (__any_sync(kFull, higher)) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const float now = fmaxf(m[h], top[h]);
+                    const float f = now == -INFINITY ? 1.0f : ex2_approx(m[h] - now);
+                    m[h] = now;
+                    l[h] *= f;
+                    const float f0 = __shfl_sync(kFull, f, quad * 8), f1 = __shfl_sync(kFull, f, quad * 8 + 4);
+#pragma unroll
+                    for (int d = 0; d < kD16; ++d) {
+                        o[d][h][0] *= f0;
+                        o[d][h][1] *= f1;
+                        o[d][h][2] *= f0;
+                        o[d][h][3] *= f1;
                     }
-                bool more = false;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
-                    more |= top[h] > m[h];
                 }
-                if (__any_sync(kFull, more)) {
+            }
+            // Weights 2^(x - m). As f16 (E4M3) they are times 2^15, so that those down to 2^-39 of the
+            // largest count. As bfloat16 they are two terms, the upper half of the float and what it
+            // leaves (one alone would cost as much as the output's own rounding); the second is never 0,
+            // so that an infinite value does not become NaN by it.
+            uint32_t p[NH][kTiles8], lo[NH][kTiles8];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float now = fmaxf(m[h], top[h]);
-                        const float f = now == -INFINITY ? 1.0f : ex2_approx(m[h] - now);
-                        m[h] = now;
-                        l[h] *= f;
+            for (int h = 0; h < NH; ++h) {
+                const float base = (m[h] == -INFINITY ? 0.0f : m[h]) - (E4M3 ? 15.0f : 0.0f);
 #pragma unroll
-                        for (int d = 0; d < D / 8; ++d) {
-                            o[d][2 * h] *= f;
-                            o[d][2 * h + 1] *= f;
-                        }
+                for (int n = 0; n < kTiles8; ++n) {
+                    const float p0 = ex2_approx(x[n][2 * h] - base), p1 = ex2_approx(x[n][2 * h + 1] - base);
+                    l[h] += p0 + p1;
+                    if constexpr (E4M3) {
+                        p[h][n] = pack_f16x2(p0, p1);
+                    } else {
+                        p[h][n] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                        lo[h][n] = pack_bf16x2(fmaxf(p0 - bf16_lo(p[h][n]), 1.2e-38f), fmaxf(p1 - bf16_hi(p[h][n]), 1.2e-38f));
                     }
                 }
-                // weights 2^(x - m); for f16 times 2^15, so that those down to 2^-39 of the largest count
-                float base[2];
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) base[h] = (m[h] == -INFINITY ? 0.0f : m[h]) - (E4M3 ? 15.0f : 0.0f);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        x[n][z] = ex2_approx(x[n][z] - base[z >> 1]);
-                        l[z >> 1] += x[n][z];
-                    }
+            for (int t = 0; t < kStep; t += 16) {
                 if constexpr (!E4M3) {
-                    // two bfloat16 terms: the upper half of the float, and what it leaves. (One alone
-                    // would cost as much as the output's own rounding.) The rest is never 0, so that
-                    // an infinite value does not become NaN by it.
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = x[i >> 1][2 * (i & 1)], p1 = x[i >> 1][2 * (i & 1) + 1];
-                        const uint32_t u0 = __float_as_uint(p0) & 0xffff0000u, u1 = __float_as_uint(p1) & 0xffff0000u;
-                        hi[i] = (u0 >> 16) | u1;
-                        lo[i] = pack_bf16x2(fmaxf(p0 - __uint_as_float(u0), 1.2e-38f), fmaxf(p1 - __uint_as_float(u1), 1.2e-38f));
-                    }
-                    const int row = lane % 16, v = lane >> 4;
+                    const int row = t + lane % 8 + (lane & 16) / 2, v = (lane >> 3) & 1;
 #pragma unroll
                     for (int d = 0; d < kD16; ++d) {
                         uint32_t r[4];
                         ldsm_t(r, vs + T::at(row, 2 * d + v));
-                        mma<false>(o[2 * d], hi, r[0], r[1]);
-                        mma<false>(o[2 * d + 1], hi, r[2], r[3]);
-                        mma<false>(o[2 * d], lo, r[0], r[1]);
-                        mma<false>(o[2 * d + 1], lo, r[2], r[3]);
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            mma<false>(o[d][h], r, p[h][t / 8], p[h][t / 8 + 1]);
+                            mma<false>(o[d][h], r, lo[h][t / 8], lo[h][t / 8 + 1]);
+                        }
                     }
                 } else {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = pack_f16x2(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1]);
-                    // A transposed 16-bit unit is two columns' bytes: even columns make one product, odd ones another.
-                    const int row = lane % 16, v = lane >> 4;
+                    // A transposed 16-bit unit is two columns' bytes: row g is column 2 g, row g + 8 column 2 g + 1.
+                    const int row = t + lane % 16, v = lane >> 4;
 #pragma unroll
                     for (int d = 0; d < kD16; d += 2) {
                         uint32_t r[4];
                         ldsm_t(r, vs + T::at(row, d + v));
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const uint32_t r0 = r[2 * z], r1 = r[2 * z + 1];
-                            mma<true>(o[2 * (d + z)], p, e4m3x2_to_f16x2(__byte_perm(r0, 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(r1, 0, 0x4420)));
-                            mma<true>(o[2 * (d + z) + 1], p, e4m3x2_to_f16x2(__byte_perm(r0, 0, 0x4431)), e4m3x2_to_f16x2(__byte_perm(r1, 0, 0x4431)));
+                            const uint32_t w0 = r[2 * z], w1 = r[2 * z + 1];
+                            const uint32_t f[4] = {e4m3x2_to_f16x2(__byte_perm(w0, 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(w0, 0, 0x4431)),
+                                                   e4m3x2_to_f16x2(__byte_perm(w1, 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(w1, 0, 0x4431))};
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) mma<true>(o[d + z][h], f, p[h][t / 8], p[h][t / 8 + 1]);
                         }
                     }
                 }
             }
-            cp_wait<0>();
-            __syncwarp();
         }
 
-        // this warp's result where its ring was
-        float* const mine = reinterpret_cast<float*>(ring);
+        // this warp's result into the stage that no load is on its way to
+        __syncwarp();
+        float* const mine = reinterpret_cast<float*>(ring + (stage == 0 ? kStages - 1 : stage - 1) * T::kStage);
+        if (lane == 0) s_out[warp] = mine;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < NH; ++h) {
             l[h] += __shfl_xor_sync(kFull, l[h], 1);
             l[h] += __shfl_xor_sync(kFull, l[h], 2);
-            const int r = g + 8 * h;
-            if (r < rows) {
-                if (quad == 0) {
-                    s_m[warp][r] = m[h];
-                    s_l[warp][r] = l[h];
-                }
-#pragma unroll
-                for (int d = 0; d < kD16; ++d) {
-                    if constexpr (!E4M3) {
-                        *reinterpret_cast<float2*>(mine + r * T::kPitch + d * 16 + quad * 2) = make_float2(o[2 * d][2 * h], o[2 * d][2 * h + 1]);
-                        *reinterpret_cast<float2*>(mine + r * T::kPitch + d * 16 + 8 + quad * 2) =
-                            make_float2(o[2 * d + 1][2 * h], o[2 * d + 1][2 * h + 1]);
-                    } else {
-                        *reinterpret_cast<float4*>(mine + r * T::kPitch + d * 16 + quad * 4) =
-                            make_float4(o[2 * d][2 * h], o[2 * d + 1][2 * h], o[2 * d][2 * h + 1], o[2 * d + 1][2 * h + 1]);
-                    }
-                }
+            if (quad == 0) {
+                s_m[warp][g + 8 * h] = m[h];
+                s_l[warp][g + 8 * h] = l[h];
             }
+#pragma unroll
+            for (int d = 0; d < kD16; ++d)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int col = E4M3 ? d * 16 + 2 * g + (z >> 1) : d * 16 + g + 8 * (z >> 1);
+                    mine[T::out_at(8 * h + 2 * quad + (z & 1), col)] = o[d][h][z];
+                }
         }
         __syncthreads();
-        const bool begins = local == 0, ends = local + seg == s.tiles;
+        const int seg = c.tiles();
+        const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles;
         const int64_t slot = 2 * int64_t(blockIdx.x) + (begins ? 1 : 0);
         for (int i = threadIdx.x; i < rows * (D / 4); i += kNt) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -496,7 +584,7 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ex2_approx(s_m[w][r] - base);
-                const float4 z = *reinterpret_cast<const float4*>(smem + w * T::kRing + (r * T::kPitch + d) * 4);
+                const float4 z = *reinterpret_cast<const float4*>(s_out[w] + T::out_at(r, d));
                 sum += f * s_l[w][r];
                 y.x += f * z.x;
                 y.y += f * z.y;
@@ -504,7 +592,7 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
                 y.w += f * z.w;
             }
             if (begins && ends) {
-                const int64_t row = int64_t(b) * a.q_heads + h0 + r;
+                const int64_t row = int64_t(c.b) * a.q_heads + h0 + r;
                 const float f = sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
                 *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
                 if (a.lse != nullptr && d == 0) a.lse[row] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
@@ -516,16 +604,10 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
                 }
             }
         }
-        if (begins && !ends) note = {b, unit, int((pos + s.tiles - 1) / place.run), 0};
-        __syncthreads();   // the rings may be filled again
-
+        if (begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), 0};
+        __syncthreads();   // the stages may be filled again
         pos += seg;
-        local = 0;
-        if (++unit == units && pos < end) {
-            unit = 0;
-            do s = span_of(a, ++b);
-            while (s.tiles == 0);
-        }
+        c.next_unit(a, units);
     }
     if (threadIdx.x == 0) ws.notes[blockIdx.x] = note;
 }
@@ -602,27 +684,36 @@ __global__ void __launch_bounds__(kNt) join_kernel(const AttentionArgs a, int gr
     }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NH>
 cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
+    using T = Tile<D, E4M3>;
     static SmemGrant grant;
-    auto kernel = attention_kernel<D, E4M3>;
-    constexpr int smem = Tile<D, E4M3>::kSmem;
+    auto kernel = attention_kernel<D, E4M3, NH>;
     cudaError_t err = grant.ensure(kernel);
     if (err != cudaSuccess) return err;
     static const int occ = [&] {
         int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNt, smem) == cudaSuccess && n > 0 ? n : 1;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNt, T::kSmem) == cudaSuccess && n > 0 ? n : 1;
     }();
     const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows;
     // no more blocks than the most tiles that these tables can hold need
-    const int64_t most = (((int64_t(a.max_pages) << a.cache.page_shift) + kTile - 1) / kTile + 1) * a.cache.heads * groups * a.B;
-    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, (most + kMinTiles - 1) / kMinTiles})));
-    err = launch_pdl(kernel, dim3(blocks), dim3(kNt), smem, stream, a, groups);
+    const int64_t tiles = ((int64_t(a.max_pages) << a.cache.page_shift) + T::kTile - 1) / T::kTile + 1;
+    const int64_t most = (tiles * a.cache.heads * groups * a.B + kMinTiles - 1) / kMinTiles;
+    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, most})));
+    err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups);
     if (err != cudaSuccess) return err;
     // few units: each is split many times, so its rows are joined by a block each
     const int64_t all = int64_t(a.B) * a.cache.heads * groups;
     const int y = all * 4 <= blocks ? unit_rows(group) : 1;
     return launch_pdl(join_kernel<D, E4M3>, dim3(blocks, y), dim3(kNt), 0, stream, a, groups, blocks);
+}
+
+// Up to 8 heads of a group make one half of a product's rows.
+template <int D>
+cudaError_t launch_heads(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
+    const bool one = a.q_heads / a.cache.heads <= 8;
+    if (a.cache.e4m3) return one ? launch_d<D, true, 1>(a, num_sms, stream) : launch_d<D, true, 2>(a, num_sms, stream);
+    return one ? launch_d<D, false, 1>(a, num_sms, stream) : launch_d<D, false, 2>(a, num_sms, stream);
 }
 
 }  // namespace
@@ -634,9 +725,9 @@ size_t paged_attention_workspace(int64_t, int q_heads, int heads, int head_dim) 
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     switch (a.cache.head_dim) {
-        case 64: return a.cache.e4m3 ? launch_d<64, true>(a, num_sms, stream) : launch_d<64, false>(a, num_sms, stream);
-        case 128: return a.cache.e4m3 ? launch_d<128, true>(a, num_sms, stream) : launch_d<128, false>(a, num_sms, stream);
-        case 256: return a.cache.e4m3 ? launch_d<256, true>(a, num_sms, stream) : launch_d<256, false>(a, num_sms, stream);
+        case 64: return launch_heads<64>(a, num_sms, stream);
+        case 128: return launch_heads<128>(a, num_sms, stream);
+        case 256: return launch_heads<256>(a, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }
