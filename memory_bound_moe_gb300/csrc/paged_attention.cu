@@ -7,7 +7,7 @@
 // cache bounds it, and mma.sync keeps up with HBM at a quarter of its rate; a
 // 128-row tcgen05 tile would be empty to seven eighths or more.
 //
-// Split. A unit of work is (sequence, key head, group of 16 heads). All units'
+// Split. A unit of work is (sequence, key heads side by side, group of 16 heads). All units'
 // tiles, one after another, are cut into equal runs, one per resident block:
 // whatever the lengths are, every SM reads the same number of bytes (the
 // lengths are on the GPU, so every block adds them up for itself). A unit
@@ -15,10 +15,10 @@
 // another run goes to the workspace (at most two per run), and a second kernel
 // joins those in order of the runs.
 //
-// A block's 4 warps take a step (16 or 32 tokens) of a tile each and never meet
-// inside a unit: each has its own ring of kStages steps in shared memory, filled
+// A block's 4 warps read up to 4 key heads of the same tokens, or steps (16 or 32
+// tokens) in turn of fewer heads, and never meet inside a unit: each has its own ring of kStages steps in shared memory, filled
 // by 16-byte cp.async, and its own running maximum, sum and output (online
-// softmax); the four are joined when the run leaves the unit. The ring goes on
+// softmax); warps of the same head are joined when the run leaves the unit. The ring goes on
 // over the units: the next ones' first steps are on their way while one is
 // finished, in the stage that was read last.
 #include "few_device.cuh"
@@ -48,24 +48,29 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // ---------------------------------------------------------------------------
 
 struct Note {
-    int32_t b, unit, last, pad;   // b < 0: none; last: the unit's last run
+    int32_t b, unit, last, run;   // b < 0: none; the unit's last and first run
 };
 
 struct Partials {
-    float* o;      // [2 blocks][rows][D], weighted by 2^(x - m)
-    float* m;      // [2 blocks][rows], log2 units
-    float* l;      // [2 blocks][rows]
+    float* o;      // [2 blocks][heads at once][rows][D], weighted by 2^(x - m)
+    float* m;      // [2 blocks][heads at once][kRows], log2 units
+    float* l;      // the same
     Note* notes;   // [blocks]
 };
 
+// Key heads that a block's warps read side by side: a token's heads lie beside
+// each other in most caches, so its bytes are asked for together, and warps of
+// different heads have nothing to join.
+inline int heads_at_once(int heads) { return heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1; }
+
 __host__ __device__ inline int unit_rows(int group) { return group < kRows ? group : kRows; }
 
-__host__ __device__ inline Partials partials(void* ws, int blocks, int rows, int D) {
+__host__ __device__ inline Partials partials(void* ws, int results, int rows, int D) {   // results: blocks times heads at once
     Partials p;
     p.o = static_cast<float*>(ws);
-    p.m = p.o + int64_t(2) * blocks * rows * D;
-    p.l = p.m + int64_t(2) * blocks * kRows;
-    p.notes = reinterpret_cast<Note*>(p.l + int64_t(2) * blocks * kRows);
+    p.m = p.o + int64_t(2) * results * rows * D;
+    p.l = p.m + int64_t(2) * results * kRows;
+    p.notes = reinterpret_cast<Note*>(p.l + int64_t(2) * results * kRows);
     return p;
 }
 
@@ -128,35 +133,33 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 // The tokens of a sequence, and where a run begins
 // ---------------------------------------------------------------------------
 
-// TILE tokens to a tile, counted from the one that holds `first`.
+// A tile is 2^ts tokens; they are counted from the one that holds `first`.
 struct Span {
     int first, len, tiles;   // tokens first .. len - 1
 };
 
-template <int TILE>
-__device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int b, int ts) {
     Span s;
     const int64_t most = int64_t(a.max_pages) << a.cache.page_shift;
     s.len = int(min(int64_t(max(__ldg(a.lengths + b), 0)), most));
     s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
-    s.tiles = s.len == 0 ? 0 : (s.len - 1) / TILE + 1 - s.first / TILE;
+    s.tiles = s.len == 0 ? 0 : ((s.len - 1) >> ts) + 1 - (s.first >> ts);
     return s;
 }
 
 // A place in a run: `left` tiles of it from tile `local` of unit `unit` of
 // sequence b on.
-template <int TILE>
 struct Cursor {
     int64_t left;
     int b, unit, local;
     Span s;
     __device__ __forceinline__ int tiles() const { return int(min(int64_t(s.tiles - local), left)); }   // of this unit
-    __device__ __forceinline__ void next_unit(const AttentionArgs& a, int units) {
+    __device__ __forceinline__ void next_unit(const AttentionArgs& a, int units, int ts) {
         left -= tiles();
         local = 0;
         if (++unit == units && left > 0) {
             unit = 0;
-            do s = span_of<TILE>(a, ++b);
+            do s = span_of(a, ++b, ts);
             while (s.tiles == 0);
         }
     }
@@ -165,15 +168,14 @@ struct Cursor {
 // This block's run. Every block adds up the sequences' tiles for itself. A
 // thread's sequences are a run of them, so that the thread in whose range this
 // block's run begins can walk to its sequence. `run`: tiles of a run.
-template <int TILE>
-__device__ __forceinline__ Cursor<TILE> find_run(const AttentionArgs& a, int units, int64_t& run) {
+__device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, int ts, int64_t& run) {
     __shared__ int64_t s_warp[kWarps];
     __shared__ int64_t s_base;
     __shared__ int s_b;
     const int per = (a.B + kNt - 1) / kNt, b0 = min(a.B, int(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     int64_t sum = 0;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) sum += span_of<TILE>(a, b).tiles;
+    for (int b = b0; b < b1; ++b) sum += span_of(a, b, ts).tiles;
     sum *= units;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     int64_t x = sum;
@@ -194,20 +196,20 @@ __device__ __forceinline__ Cursor<TILE> find_run(const AttentionArgs& a, int uni
     const int64_t start = run * blockIdx.x;
     if (before <= start && start < before + sum) {
         int b = b0;
-        int64_t n = int64_t(span_of<TILE>(a, b).tiles) * units;
+        int64_t n = int64_t(span_of(a, b, ts).tiles) * units;
         while (before + n <= start) {
             before += n;
-            n = int64_t(span_of<TILE>(a, ++b).tiles) * units;
+            n = int64_t(span_of(a, ++b, ts).tiles) * units;
         }
         s_base = before;
         s_b = b;
     }
     __syncthreads();
-    Cursor<TILE> c = {};
+    Cursor c = {};
     c.left = max(int64_t(0), min(run, total - start));
     if (c.left > 0) {
         c.b = s_b;
-        c.s = span_of<TILE>(a, c.b);
+        c.s = span_of(a, c.b, ts);
         c.unit = int((start - s_base) / c.s.tiles);
         c.local = int((start - s_base) % c.s.tiles);
     }
@@ -220,8 +222,8 @@ __device__ __forceinline__ Cursor<TILE> find_run(const AttentionArgs& a, int uni
 
 template <int D, bool E4M3>
 struct Tile {
-    static constexpr int kStep = E4M3 || D == 64 ? 32 : 16;   // tokens of a warp's step
-    static constexpr int kTile = kWarps * kStep;
+    static constexpr int kStepLog2 = E4M3 || D == 64 ? 5 : 4;
+    static constexpr int kStep = 1 << kStepLog2;              // tokens of a warp's step
     static constexpr int kBytes = D * (E4M3 ? 1 : 2);         // of a token's head
     static constexpr int kVecs = kBytes / 16;
     static constexpr int kPer = kWarp / kVecs;                // rows that a warp copies with one instruction
@@ -279,7 +281,7 @@ __device__ __forceinline__ void load_step(uint32_t dst, const CacheView& c, cons
 }
 
 template <int D, bool E4M3, int NH>
-__global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, int groups) {
+__global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, int groups, int side) {
     using T = Tile<D, E4M3>;
     constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -287,14 +289,16 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
     __shared__ const float* s_out[kWarps];
     pdl_wait_and_release();
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, quad = lane % 4;
-    const int heads = a.cache.heads, group = a.q_heads / heads, units = heads * groups;
-    const Partials ws = partials(a.workspace, gridDim.x, unit_rows(group), D);
+    const int heads = a.cache.heads, group = a.q_heads / heads, units = heads / side * groups;
+    const int mine_head = warp % side, phase = warp / side, phases = kWarps / side;
+    const int ts = __ffs(kStep * phases) - 1;
+    const Partials ws = partials(a.workspace, gridDim.x * side, unit_rows(group), D);
     uint8_t* const ring = smem + warp * T::kRing;
     const uint32_t ring_at = uint32_t(__cvta_generic_to_shared(ring));
 
     // sequences without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (span_of<T::kTile>(a, b).tiles == 0) {
+        if (span_of(a, b, ts).tiles == 0) {
             uint4* o = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.q_heads * D);
             for (int i = threadIdx.x; i < a.q_heads * D / 8; i += kNt) o[i] = make_uint4(0, 0, 0, 0);
             if (a.lse != nullptr)
@@ -302,31 +306,31 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
         }
 
     int64_t run = 0;
-    Cursor<T::kTile> c = find_run<T::kTile>(a, units, run);
-    // this warp's steps of a cursor's unit: tokens from + (j kWarps + warp) kStep on
-    const auto open = [&](const Cursor<T::kTile>& p, int& from) {
-        const int begin = (p.s.first / T::kTile + p.local) * T::kTile;
+    Cursor c = find_run(a, units, ts, run);
+    // this warp's steps of a cursor's unit: tokens from + (j phases + phase) kStep on
+    const auto open = [&](const Cursor& p, int& from) {
+        const int begin = ((p.s.first >> ts) + p.local) << ts;
         from = max(begin, p.s.first & ~(kStep - 1));
-        const int to = min(p.s.len, begin + p.tiles() * T::kTile);
-        return ((to - from + kStep - 1) / kStep - warp + kWarps - 1) / kWarps;
+        const int to = min(p.s.len, begin + (p.tiles() << ts));
+        return ((to - from + kStep - 1) / kStep - phase + phases - 1) >> (ts - T::kStepLog2);
     };
 
     // The loads run ahead of the products, over the units' ends: `ahead` is
     // where they are, next_t0 and next_page the step to be loaded next.
-    Cursor<T::kTile> ahead = c;
+    Cursor ahead = c;
     int ahead_from = 0, ahead_j = 0, ahead_steps = 0, next_t0 = 0, next_page = -1;
     bool more = c.left > 0;
     if (more) ahead_steps = open(ahead, ahead_from);
     const auto look = [&]() {
         while (more && ahead_j >= ahead_steps) {
-            ahead.next_unit(a, units);
+            ahead.next_unit(a, units, ts);
             more = ahead.left > 0;
             ahead_j = 0;
             if (more) ahead_steps = open(ahead, ahead_from);
         }
         next_page = -1;
         if (more) {
-            next_t0 = ahead_from + (ahead_j++ * kWarps + warp) * kStep;
+            next_t0 = ahead_from + (ahead_j++ * phases + phase) * kStep;
             const int t = next_t0 + lane % kStep;
             if (t >= ahead.s.first && t < ahead.s.len) {
                 const int pg = __ldg(a.block_table + int64_t(ahead.b) * a.max_pages + (t >> a.cache.page_shift));
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
         uint32_t mask = __ballot_sync(kFull, next_page >= 0);
         if (kStep == 16) mask &= 0xffffu;
         if (more) {
-            const int64_t head = ahead.unit / groups;
+            const int64_t head = ahead.unit / groups * side + mine_head;
             load_step<D, E4M3>(ring_at + stage * T::kStage, a.cache, a.cache.k + head * a.cache.k_head,
                                a.cache.v + head * a.cache.v_head, next_t0, next_page, mask);
         }
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
     Note note = {-1, 0, 0, 0};
     int64_t pos = run * blockIdx.x;
     while (c.left > 0) {
-        const int head = c.unit / groups, chunk = c.unit % groups;
+        const int head = c.unit / groups * side + mine_head, chunk = c.unit % groups;
         const int rows = min(kRows, group - chunk * kRows);
         const int h0 = head * group + chunk * kRows;
 
@@ -569,20 +573,17 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
                     mine[T::out_at(8 * h + 2 * quad + (z & 1), col)] = o[d][h][z];
                 }
         }
-        __syncthreads();
+        group_sync(mine_head, phases);
         const int seg = c.tiles();
         const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles;
-        const int64_t slot = 2 * int64_t(blockIdx.x) + (begins ? 1 : 0);
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kNt) {
+        const int64_t slot = (2 * int64_t(blockIdx.x) + (begins ? 1 : 0)) * side + mine_head;
+        for (int i = phase * kWarp + lane; i < rows * (D / 4); i += phases * kWarp) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
-            float most = s_m[0][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) most = fmaxf(most, s_m[w][r]);
+            float most = -INFINITY, sum = 0.0f;
+            for (int w = mine_head; w < kWarps; w += side) most = fmaxf(most, s_m[w][r]);
             const float base = most == -INFINITY ? 0.0f : most;
-            float sum = 0.0f;
             float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = mine_head; w < kWarps; w += side) {
                 const float f = ex2_approx(s_m[w][r] - base);
                 const float4 z = *reinterpret_cast<const float4*>(s_out[w] + T::out_at(r, d));
                 sum += f * s_l[w][r];
@@ -604,84 +605,128 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
                 }
             }
         }
-        if (begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), 0};
-        __syncthreads();   // the stages may be filled again
+        if (begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
+        group_sync(mine_head, phases);   // the stages may be filled again
         pos += seg;
-        c.next_unit(a, units);
+        c.next_unit(a, units, ts);
     }
     if (threadIdx.x == 0) ws.notes[blockIdx.x] = note;
 }
 
 // ---------------------------------------------------------------------------
-// Join of the units that several runs share: block x looks at the note of run
-// x, block y takes every gridDim.y-th row.
+// Join of the units that several runs share: a warp, or `warps` of them, per
+// row (unit, head). Every block gathers the notes for itself.
 // ---------------------------------------------------------------------------
 
+constexpr int kJoinWarps = 8;
+constexpr int kJoinBatch = 8;        // partial results that a warp asks for at once
+
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kNt) join_kernel(const AttentionArgs a, int groups, int blocks) {
-    constexpr int kCols = D / 4, kParts = kNt / kCols;   // float4 columns; parts added side by side
-    __shared__ float s_f[kMaxBlocks];
-    __shared__ float s_red[2][kWarps];
-    __shared__ float4 s_o[kParts][kCols];
+__global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const AttentionArgs a, int groups, int side, int blocks, int warps) {
+    constexpr int kLanes = D == 64 ? 16 : 32, kVecs = D / (4 * kLanes), kSub = kWarp / kLanes;   // lanes of a row; rows side by side
+    __shared__ Note s_note[kMaxBlocks];
+    __shared__ int s_count[kJoinWarps];
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ float4 s_o[kJoinWarps][D / 4];
     pdl_wait_and_release();
-    const int heads = a.cache.heads, group = a.q_heads / heads, run = blockIdx.x;
-    const Partials ws = partials(a.workspace, blocks, unit_rows(group), D);
-    const Note note = ws.notes[run];
-    if (note.b < 0) return;
-    const int head = note.unit / groups, chunk = note.unit % groups;
-    const int rows = min(kRows, group - chunk * kRows), h0 = head * group + chunk * kRows;
-    const int parts = note.last - run + 1, warp = threadIdx.x / kWarp;
-    const auto slot_of = [&](int i) { return i == 0 ? 2 * int64_t(run) + 1 : 2 * int64_t(run + i); };
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        float most = -INFINITY;
-        for (int i = threadIdx.x; i < parts; i += kNt) most = fmaxf(most, ws.m[slot_of(i) * kRows + r]);
-#pragma unroll
-        for (int o = kWarp / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-        if (threadIdx.x % kWarp == 0) s_red[0][warp] = most;
+    const int heads = a.cache.heads, group = a.q_heads / heads, urows = unit_rows(group), rows_all = side * urows;
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    const Partials ws = partials(a.workspace, blocks * side, urows, D);
+    int units = 0;
+    for (int r0 = 0; r0 < blocks; r0 += kJoinWarps * kWarp) {
+        const int run = r0 + threadIdx.x;
+        const Note n = run < blocks ? ws.notes[run] : Note{-1, 0, 0, 0};
+        const uint32_t there = __ballot_sync(kFull, n.b >= 0);
+        if (lane == 0) s_count[warp] = __popc(there);
         __syncthreads();
+        int at = units + __popc(there & ((1u << lane) - 1u));
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) most = fmaxf(most, s_red[0][w]);
-        const float base = most == -INFINITY ? 0.0f : most;
-        float sum = 0.0f;
-        for (int i = threadIdx.x; i < parts; i += kNt) {
-            const float f = ex2_approx(ws.m[slot_of(i) * kRows + r] - base);
-            s_f[i] = f;
-            sum += f * ws.l[slot_of(i) * kRows + r];
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w < warp) at += s_count[w];
+            units += s_count[w];
         }
-#pragma unroll
-        for (int o = kWarp / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (threadIdx.x % kWarp == 0) s_red[1][warp] = sum;
+        if (n.b >= 0) s_note[at] = n;
         __syncthreads();
-        sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_red[1][w];
-        const int d = threadIdx.x % kCols, p0 = threadIdx.x / kCols;
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int i = p0; i < parts; i += kParts) {
-            const float f = s_f[i];
-            const float4 z = *reinterpret_cast<const float4*>(ws.o + (slot_of(i) * unit_rows(group) + r) * D + d * 4);
-            y.x += f * z.x;
-            y.y += f * z.y;
-            y.z += f * z.z;
-            y.w += f * z.w;
-        }
-        s_o[p0][d] = y;
-        __syncthreads();
-        if (p0 == 0) {
-            for (int i = 1; i < kParts; ++i) {
-                y.x += s_o[i][d].x;
-                y.y += s_o[i][d].y;
-                y.z += s_o[i][d].z;
-                y.w += s_o[i][d].w;
-            }
-            const int64_t row = int64_t(note.b) * a.q_heads + h0 + r;
-            const float f = sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
-            *reinterpret_cast<uint2*>(a.out + row * D + d * 4) = make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-            if (a.lse != nullptr && d == 0) a.lse[row] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
-        }
-        __syncthreads();   // s_f, s_red and s_o are used again
     }
+    const int item = (int(blockIdx.x) * kJoinWarps + warp) / warps, sub = warp % warps;
+    const int r = item % urows, side_head = item % rows_all / urows;
+    const bool in = item < units * rows_all;
+    const Note n = in ? s_note[item / rows_all] : Note{};
+    const int chunk = n.unit % groups, head = n.unit / groups * side + side_head;
+    const bool valid = in && r < group - chunk * kRows;   // the last group of 16 may be smaller
+    const int parts = valid ? n.last - n.run + 1 : 0;
+    float m = -INFINITY, l = 0.0f;
+    float4 y[kVecs] = {};
+    const auto add = [&](float m1, float l1, const float4 (&z)[kVecs]) {
+        const float now = fmaxf(m, m1), base = now == -INFINITY ? 0.0f : now;
+        const float f = ex2_approx(m - base), f1 = ex2_approx(m1 - base);
+        m = now;
+        l = l * f + l1 * f1;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            y[v].x = y[v].x * f + z[v].x * f1;
+            y[v].y = y[v].y * f + z[v].y * f1;
+            y[v].z = y[v].z * f + z[v].z * f1;
+            y[v].w = y[v].w * f + z[v].w * f1;
+        }
+    };
+    const int step = warps * kSub;
+    for (int p0 = sub * kSub + lane / kLanes; p0 - lane / kLanes < parts; p0 += step * kJoinBatch) {
+        float m1[kJoinBatch], l1[kJoinBatch];
+        float4 z[kJoinBatch][kVecs];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const int p = p0 + i * step;
+            m1[i] = -INFINITY;
+            l1[i] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) z[i][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p < parts) {
+                const int64_t slot = (2 * int64_t(n.run + p) + (p == 0 ? 1 : 0)) * side + side_head;
+                m1[i] = ws.m[slot * kRows + r];
+                l1[i] = ws.l[slot * kRows + r];
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+                    z[i][v] = reinterpret_cast<const float4*>(ws.o + (slot * urows + r) * D)[lane % kLanes + v * kLanes];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) add(m1[i], l1[i], z[i]);
+    }
+    if constexpr (kSub == 2) {
+        float4 z[kVecs];
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            z[v] = make_float4(__shfl_xor_sync(kFull, y[v].x, 16), __shfl_xor_sync(kFull, y[v].y, 16),
+                               __shfl_xor_sync(kFull, y[v].z, 16), __shfl_xor_sync(kFull, y[v].w, 16));
+        add(__shfl_xor_sync(kFull, m, 16), __shfl_xor_sync(kFull, l, 16), z);
+    }
+    if (warps > 1) {
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_l[warp] = l;
+        }
+        if (lane < kLanes)
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) s_o[warp][lane + v * kLanes] = y[v];
+        __syncthreads();
+        if (sub == 0)
+            for (int w = 1; w < warps; ++w) {
+                float4 z[kVecs];
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v) z[v] = s_o[warp + w][lane % kLanes + v * kLanes];
+                add(s_m[warp + w], s_l[warp + w], z);
+            }
+    }
+    if (!valid || sub != 0) return;
+    const int64_t row = int64_t(n.b) * a.q_heads + head * group + chunk * kRows + r;
+    const float f = l == 0.0f ? 0.0f : a.cache.v_scale / l;
+    if (lane < kLanes)
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            *reinterpret_cast<uint2*>(a.out + row * D + (lane + v * kLanes) * 4) =
+                make_uint2(pack_bf16x2(y[v].x * f, y[v].y * f), pack_bf16x2(y[v].z * f, y[v].w * f));
+    if (a.lse != nullptr && lane == 0) a.lse[row] = (m + log2f(l) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
 }
 
 template <int D, bool E4M3, int NH>
@@ -695,17 +740,24 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
         int n = 0;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNt, T::kSmem) == cudaSuccess && n > 0 ? n : 1;
     }();
-    const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows;
+    const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows, side = heads_at_once(a.cache.heads);
     // no more blocks than the most tiles that these tables can hold need
-    const int64_t tiles = ((int64_t(a.max_pages) << a.cache.page_shift) + T::kTile - 1) / T::kTile + 1;
-    const int64_t most = (tiles * a.cache.heads * groups * a.B + kMinTiles - 1) / kMinTiles;
+    const int tile = kWarps / side * T::kStep;
+    const int64_t tiles = ((int64_t(a.max_pages) << a.cache.page_shift) + tile - 1) / tile + 1;
+    const int64_t most = (tiles * (a.cache.heads / side) * groups * a.B + kMinTiles - 1) / kMinTiles;
     const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, most})));
-    err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups);
+    err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups, side);
     if (err != cudaSuccess) return err;
-    // few units: each is split many times, so its rows are joined by a block each
-    const int64_t all = int64_t(a.B) * a.cache.heads * groups;
-    const int y = all * 4 <= blocks ? unit_rows(group) : 1;
-    return launch_pdl(join_kernel<D, E4M3>, dim3(blocks, y), dim3(kNt), 0, stream, a, groups, blocks);
+    // Units that may be split: all of them, or the one at each border of two runs. A row of one
+    // gets a warp for every 8 of the runs that share it on average.
+    const int64_t all = int64_t(a.B) * (a.cache.heads / side) * groups;
+    const int split = int(std::min<int64_t>(blocks - 1, all));
+    if (split == 0) return cudaSuccess;
+    int warps = 1;
+    while (warps < kJoinWarps && blocks > split * warps * kJoinBatch) warps *= 2;
+    const int64_t join_warps = int64_t(split) * side * unit_rows(group) * warps;
+    return launch_pdl(join_kernel<D, E4M3>, dim3(unsigned((join_warps + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * kWarp), 0,
+                      stream, a, groups, side, blocks, warps);
 }
 
 // Up to 8 heads of a group make one half of a product's rows.
@@ -720,7 +772,7 @@ cudaError_t launch_heads(const AttentionArgs& a, int num_sms, cudaStream_t strea
 
 size_t paged_attention_workspace(int64_t, int q_heads, int heads, int head_dim) {
     const size_t rows = size_t(unit_rows(q_heads / heads));
-    return size_t(2 * kMaxBlocks) * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
+    return size_t(2 * kMaxBlocks * heads_at_once(heads)) * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
