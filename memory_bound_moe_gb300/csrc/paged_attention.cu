@@ -30,11 +30,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kNt = kWarps * kWarp;
 constexpr int kRows = 16;            // query heads of a unit, at most
-#ifndef MOE_ATTN_STAGES
-#define MOE_ATTN_STAGES 3
+#ifndef MOE_ATTN_WAVES
+#define MOE_ATTN_WAVES 1
 #endif
-constexpr int kStages = MOE_ATTN_STAGES;
-constexpr int kMaxBlocks = 640;      // runs the workspace holds the ends of
+#ifndef MOE_ATTN_MAXB
+#define MOE_ATTN_MAXB 640
+#endif
+constexpr int kMaxBlocks = MOE_ATTN_MAXB;      // runs the workspace holds the ends of
 #ifndef MOE_ATTN_MIN_TILES
 #define MOE_ATTN_MIN_TILES 2
 #endif
@@ -229,6 +231,8 @@ struct Tile {
     static constexpr int kPer = kWarp / kVecs;                // rows that a warp copies with one instruction
     static constexpr int kSide = kStep * kBytes;              // keys or values of a step
     static constexpr int kStage = 2 * kSide;
+    static constexpr int kBlocks = D == 256 ? 1 : D == 128 && !E4M3 ? 2 : 3;   // of an SM
+    static constexpr int kStages = kBlocks == 3 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;            // of a warp
     static constexpr int kSmem = kWarps * kRing;
     static_assert(kRows * D * 4 <= kStage, "a warp's output takes the place of a stage");
@@ -281,11 +285,11 @@ __device__ __forceinline__ void load_step(uint32_t dst, const CacheView& c, cons
 }
 
 template <int D, bool E4M3, int NH>
-__global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, int groups, int side) {
+__global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(const AttentionArgs a, int groups, int side) {
     using T = Tile<D, E4M3>;
-    constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8;
+    constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8, kStages = T::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_f[kWarps][kRows];
     __shared__ const float* s_out[kWarps];
     pdl_wait_and_release();
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, quad = lane % 4;
@@ -295,15 +299,6 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
     const Partials ws = partials(a.workspace, gridDim.x * side, unit_rows(group), D);
     uint8_t* const ring = smem + warp * T::kRing;
     const uint32_t ring_at = uint32_t(__cvta_generic_to_shared(ring));
-
-    // sequences without tokens
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (span_of(a, b, ts).tiles == 0) {
-            uint4* o = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.q_heads * D);
-            for (int i = threadIdx.x; i < a.q_heads * D / 8; i += kNt) o[i] = make_uint4(0, 0, 0, 0);
-            if (a.lse != nullptr)
-                for (int i = threadIdx.x; i < a.q_heads; i += kNt) a.lse[int64_t(b) * a.q_heads + i] = -INFINITY;
-        }
 
     int64_t run = 0;
     Cursor c = find_run(a, units, ts, run);
@@ -355,6 +350,15 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
 #pragma unroll
     for (int i = 0; i + 1 < kStages; ++i) masks[i] = issue(i);
     int stage = 0;             // of the step that comes next
+
+    // sequences without tokens
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (span_of(a, b, ts).tiles == 0) {
+            uint4* o = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.q_heads * D);
+            for (int i = threadIdx.x; i < a.q_heads * D / 8; i += kNt) o[i] = make_uint4(0, 0, 0, 0);
+            if (a.lse != nullptr)
+                for (int i = threadIdx.x; i < a.q_heads; i += kNt) a.lse[int64_t(b) * a.q_heads + i] = -INFINITY;
+        }
 
     Note note = {-1, 0, 0, 0};
     int64_t pos = run * blockIdx.x;
@@ -577,33 +581,39 @@ __global__ void __launch_bounds__(kNt) attention_kernel(const AttentionArgs a, i
         const int seg = c.tiles();
         const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles;
         const int64_t slot = (2 * int64_t(blockIdx.x) + (begins ? 1 : 0)) * side + mine_head;
-        for (int i = phase * kWarp + lane; i < rows * (D / 4); i += phases * kWarp) {
-            const int r = i / (D / 4), d = i % (D / 4) * 4;
+        // what a warp's row counts in the sum of the head's warps, and for a whole unit in the output
+        for (int r = phase * kWarp + lane; r < rows; r += phases * kWarp) {
             float most = -INFINITY, sum = 0.0f;
             for (int w = mine_head; w < kWarps; w += side) most = fmaxf(most, s_m[w][r]);
             const float base = most == -INFINITY ? 0.0f : most;
+            for (int w = mine_head; w < kWarps; w += side) sum += ex2_approx(s_m[w][r] - base) * s_l[w][r];
+            const float inv = !(begins && ends) ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+            for (int w = mine_head; w < kWarps; w += side) s_f[w][r] = ex2_approx(s_m[w][r] - base) * inv;
+            if (!(begins && ends)) {
+                ws.m[slot * kRows + r] = most;
+                ws.l[slot * kRows + r] = sum;
+            } else if (a.lse != nullptr) {
+                a.lse[int64_t(c.b) * a.q_heads + h0 + r] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
+            }
+        }
+        group_sync(mine_head, phases);
+#pragma unroll 2
+        for (int i = phase * kWarp + lane; i < rows * (D / 4); i += phases * kWarp) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
             float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int w = mine_head; w < kWarps; w += side) {
-                const float f = ex2_approx(s_m[w][r] - base);
+                const float f = s_f[w][r];
                 const float4 z = *reinterpret_cast<const float4*>(s_out[w] + T::out_at(r, d));
-                sum += f * s_l[w][r];
                 y.x += f * z.x;
                 y.y += f * z.y;
                 y.z += f * z.z;
                 y.w += f * z.w;
             }
-            if (begins && ends) {
-                const int64_t row = int64_t(c.b) * a.q_heads + h0 + r;
-                const float f = sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
-                *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-                if (a.lse != nullptr && d == 0) a.lse[row] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
-            } else {
+            if (begins && ends)
+                *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
+                    make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            else
                 *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
-                if (d == 0) {
-                    ws.m[slot * kRows + r] = most;
-                    ws.l[slot * kRows + r] = sum;
-                }
-            }
         }
         if (begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
         group_sync(mine_head, phases);   // the stages may be filled again
@@ -745,7 +755,7 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     const int tile = kWarps / side * T::kStep;
     const int64_t tiles = ((int64_t(a.max_pages) << a.cache.page_shift) + tile - 1) / tile + 1;
     const int64_t most = (tiles * (a.cache.heads / side) * groups * a.B + kMinTiles - 1) / kMinTiles;
-    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, most})));
+    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ * MOE_ATTN_WAVES, kMaxBlocks, most})));
     err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups, side);
     if (err != cudaSuccess) return err;
     // Units that may be split: all of them, or the one at each border of two runs. A row of one
