@@ -30,17 +30,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kNt = kWarps * kWarp;
 constexpr int kRows = 16;            // query heads of a unit, at most
-#ifndef MOE_ATTN_WAVES
-#define MOE_ATTN_WAVES 1
-#endif
-#ifndef MOE_ATTN_MAXB
-#define MOE_ATTN_MAXB 640
-#endif
-constexpr int kMaxBlocks = MOE_ATTN_MAXB;      // runs the workspace holds the ends of
-#ifndef MOE_ATTN_MIN_TILES
-#define MOE_ATTN_MIN_TILES 2
-#endif
-constexpr int kMinTiles = MOE_ATTN_MIN_TILES;   // tiles of a run, at least
+constexpr int kMaxBlocks = 640;      // runs the workspace holds the ends of
+constexpr int kMinTiles = 2;         // tiles of a run, at least
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // ---------------------------------------------------------------------------
@@ -284,13 +275,25 @@ __device__ __forceinline__ void load_step(uint32_t dst, const CacheView& c, cons
     }
 }
 
+constexpr int kMaxRanks = 8;   // blocks of a cluster: the portable limit
+
+__device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
+    const uint32_t a = uint32_t(__cvta_generic_to_shared(p));
+    uint32_t r;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(r) : "memory");
+    return v;
+}
+
 template <int D, bool E4M3, int NH>
-__global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(const AttentionArgs a, int groups, int side) {
+__global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(const AttentionArgs a, int groups, int side, int ranks) {
     using T = Tile<D, E4M3>;
     constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8, kStages = T::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_f[kWarps][kRows];
     __shared__ const float* s_out[kWarps];
+    __shared__ float s_cm[kRows], s_cl[kRows];   // this block's share of a cluster's unit
     pdl_wait_and_release();
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, quad = lane % 4;
     const int heads = a.cache.heads, group = a.q_heads / heads, units = heads / side * groups;
@@ -298,10 +301,29 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
     const int ts = __ffs(kStep * phases) - 1;
     const Partials ws = partials(a.workspace, gridDim.x * side, unit_rows(group), D);
     uint8_t* const ring = smem + warp * T::kRing;
+    float* const s_co = reinterpret_cast<float*>(smem + T::kSmem);   // [rows][D], for clusters alone
     const uint32_t ring_at = uint32_t(__cvta_generic_to_shared(ring));
 
     int64_t run = 0;
-    Cursor c = find_run(a, units, ts, run);
+    Cursor c = {};
+    const int rank = ranks > 0 ? blockIdx.x % ranks : 0;
+    if (ranks > 0) {
+        // a cluster's unit, its tiles in equal shares
+        const int u = blockIdx.x / ranks;
+        c.b = u / units;
+        c.unit = u % units;
+        c.s = span_of(a, c.b, ts);
+        const int share = (c.s.tiles + ranks - 1) / ranks;
+        c.local = min(rank * share, c.s.tiles);
+        c.left = min(share, c.s.tiles - c.local);
+        if (threadIdx.x < kRows) {
+            s_cm[threadIdx.x] = -INFINITY;
+            s_cl[threadIdx.x] = 0.0f;
+        }
+        __syncthreads();
+    } else {
+        c = find_run(a, units, ts, run);
+    }
     // this warp's steps of a cursor's unit: tokens from + (j phases + phase) kStep on
     const auto open = [&](const Cursor& p, int& from) {
         const int begin = ((p.s.first >> ts) + p.local) << ts;
@@ -352,7 +374,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
     int stage = 0;             // of the step that comes next
 
     // sequences without tokens
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    for (int b = blockIdx.x; ranks == 0 && b < a.B; b += gridDim.x)
         if (span_of(a, b, ts).tiles == 0) {
             uint4* o = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.q_heads * D);
             for (int i = threadIdx.x; i < a.q_heads * D / 8; i += kNt) o[i] = make_uint4(0, 0, 0, 0);
@@ -579,7 +601,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
         }
         group_sync(mine_head, phases);
         const int seg = c.tiles();
-        const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles;
+        const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles, whole = begins && ends && ranks == 0;
         const int64_t slot = (2 * int64_t(blockIdx.x) + (begins ? 1 : 0)) * side + mine_head;
         // what a warp's row counts in the sum of the head's warps, and for a whole unit in the output
         for (int r = phase * kWarp + lane; r < rows; r += phases * kWarp) {
@@ -587,9 +609,12 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
             for (int w = mine_head; w < kWarps; w += side) most = fmaxf(most, s_m[w][r]);
             const float base = most == -INFINITY ? 0.0f : most;
             for (int w = mine_head; w < kWarps; w += side) sum += ex2_approx(s_m[w][r] - base) * s_l[w][r];
-            const float inv = !(begins && ends) ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+            const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
             for (int w = mine_head; w < kWarps; w += side) s_f[w][r] = ex2_approx(s_m[w][r] - base) * inv;
-            if (!(begins && ends)) {
+            if (ranks > 0) {
+                s_cm[r] = most;
+                s_cl[r] = sum;
+            } else if (!whole) {
                 ws.m[slot * kRows + r] = most;
                 ws.l[slot * kRows + r] = sum;
             } else if (a.lse != nullptr) {
@@ -609,18 +634,62 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
                 y.z += f * z.z;
                 y.w += f * z.w;
             }
-            if (begins && ends)
+            if (ranks > 0)
+                *reinterpret_cast<float4*>(s_co + r * D + d) = y;
+            else if (whole)
                 *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
                     make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
             else
                 *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
         }
-        if (begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
+        if (ranks == 0 && begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
         group_sync(mine_head, phases);   // the stages may be filled again
         pos += seg;
         c.next_unit(a, units, ts);
     }
-    if (threadIdx.x == 0) ws.notes[blockIdx.x] = note;
+    if (ranks == 0) {
+        if (threadIdx.x == 0) ws.notes[blockIdx.x] = note;
+        return;
+    }
+
+    // The blocks of a cluster join their shares: each takes some of the rows' columns.
+    cluster_sync();
+    const int u = blockIdx.x / ranks, unit = u % units, head = unit / groups, chunk = unit % groups;
+    const int rows = min(kRows, group - chunk * kRows);
+    for (int i = rank * kNt + threadIdx.x; i < rows * (D / 4); i += ranks * kNt) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float m1[kMaxRanks], l1[kMaxRanks];
+        float4 z[kMaxRanks];
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) {
+            m1[k] = -INFINITY;
+            if (k < ranks) {
+                m1[k] = ld_cluster(s_cm + r, k);
+                l1[k] = ld_cluster(s_cl + r, k);
+                z[k] = ld_cluster4(s_co + r * D + d, k);
+            }
+        }
+        float most = m1[0], sum = 0.0f;
+#pragma unroll
+        for (int k = 1; k < kMaxRanks; ++k) most = fmaxf(most, m1[k]);
+        const float base = most == -INFINITY ? 0.0f : most;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k)
+            if (m1[k] != -INFINITY) {   // a block without tokens left nothing
+                const float f = ex2_approx(m1[k] - base);
+                sum += f * l1[k];
+                y.x += f * z[k].x;
+                y.y += f * z[k].y;
+                y.z += f * z[k].z;
+                y.w += f * z[k].w;
+            }
+        const int64_t row = int64_t(u / units) * a.q_heads + head * group + chunk * kRows + r;
+        const float f = sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+        *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+        if (a.lse != nullptr && d == 0) a.lse[row] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
+    }
+    cluster_sync();   // the others may still read this block's share
 }
 
 // ---------------------------------------------------------------------------
@@ -750,13 +819,29 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
         int n = 0;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNt, T::kSmem) == cudaSuccess && n > 0 ? n : 1;
     }();
-    const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows, side = heads_at_once(a.cache.heads);
+    const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows;
+    const int64_t table = int64_t(a.max_pages) << a.cache.page_shift, longest = a.window > 0 ? std::min<int64_t>(table, a.window) : table;
+
+    // Units that are few and cannot be long go to clusters of as many blocks as find room at once (with
+    // an eighth to spare: clusters do not fit everywhere), each unit's tokens in equal shares: one kernel
+    // and no join, where the runs cost 4 to 7 us more but share uneven lengths evenly. GB300, bfloat16,
+    // D = 128, clusters against runs, in us: 8 units of 1000 tokens 7.5 / 11.9, of 4000 11.9 / 14.3, of
+    // 8000 19.8 / 17.9; 2 units of 2000 8.7 / 9.3, of 4000 11.8 / 9.5; 64 units of 1000 10.9 / 18.0, of 1
+    // to 8000 38.0 / 36.7; 256 units of 1000 27.7 / 32.4, of 1 to 4000 66.9 / 53.7. Hence at most 256 KB
+    // of keys per block, and fewer where few units leave most SMs idle.
+    const int64_t clusters = int64_t(a.B) * a.cache.heads * groups;
+    int ranks = kMaxRanks;
+    while (ranks > 0 && clusters * ranks * 8 > int64_t(num_sms) * occ * 7) ranks /= 2;
+    if (ranks > 0 && longest * T::kBytes <= ranks * std::min<int64_t>(262144, 65536 + 16384 * clusters))
+        return launch_cluster(kernel, dim3(unsigned(clusters * ranks)), dim3(kNt), ranks, T::kSmem + unit_rows(group) * D * 4,
+                              stream, a, groups, 1, ranks);
+    const int side = heads_at_once(a.cache.heads);
     // no more blocks than the most tiles that these tables can hold need
     const int tile = kWarps / side * T::kStep;
-    const int64_t tiles = ((int64_t(a.max_pages) << a.cache.page_shift) + tile - 1) / tile + 1;
+    const int64_t tiles = (longest + tile - 1) / tile + 1;
     const int64_t most = (tiles * (a.cache.heads / side) * groups * a.B + kMinTiles - 1) / kMinTiles;
-    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ * MOE_ATTN_WAVES, kMaxBlocks, most})));
-    err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups, side);
+    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, most})));
+    err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups, side, 0);
     if (err != cudaSuccess) return err;
     // Units that may be split: all of them, or the one at each border of two runs. A row of one
     // gets a warp for every 8 of the runs that share it on average.
