@@ -550,9 +550,11 @@ def _addr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int
     """The address of a tensor that is what the call needs: ``_need``, on the
     device ``dev``. (One test for the good case: these calls take a few
     microseconds on the GPU, so the host's checks are kept short.)"""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:   # no tensor
+        pass
     _need(t, name, dtype, shape)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 

@@ -128,9 +128,8 @@ __global__ void __launch_bounds__(kNt) page_table_kernel(const PageTableArgs a) 
         a.lengths[b] = s_cached[b] + (s_new[b] >= 0 ? s_end[b] - begin : 0);
     }
     // sums of the threads' counts, and the largest of their page totals
-    int64_t all = 0, before = 0;
-    before = block_before(refused, s_sum, all);
-    (void)before;
+    int64_t all = 0;
+    block_before(refused, s_sum, all);
 #pragma unroll
     for (int o = kWarp / 2; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(kFull, last, o));
     if (threadIdx.x % kWarp == 0) s_sum[threadIdx.x / kWarp] = last;

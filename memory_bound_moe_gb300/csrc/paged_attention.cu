@@ -263,15 +263,31 @@ __device__ __forceinline__ void load_step(uint32_t dst, const CacheView& c, cons
         }
         return;
     }
-    const int64_t pg = page, t = (t0 + lane % T::kStep) & in_page;   // this lane's row's, where it is valid
+    // Each lane has its row's offsets (its token's, where there is one) and the rows' lanes ask for them.
+    const int64_t pg = page, t = (t0 + lane % T::kStep) & in_page;
     const int64_t ko = pg * c.k_page + t * c.k_token, vo = pg * c.v_page + t * c.v_token;
+    k += vec * 16;
+    v += vec * 16;
+    if (mask == kAll) {
+        const bool alike = c.k_page == c.v_page && c.k_token == c.v_token;
+#pragma unroll
+        for (int i = 0; i < T::kStep; i += T::kPer) {
+            const int64_t kr = shfl64(ko, i + row);
+            cp_async16(dst + T::at(i + row, vec), k + kr);
+            if (alike) cp_async16(dst + T::kSide + T::at(i + row, vec), v + kr);
+        }
+        if (!alike)
+#pragma unroll
+            for (int i = 0; i < T::kStep; i += T::kPer) cp_async16(dst + T::kSide + T::at(i + row, vec), v + shfl64(vo, i + row));
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < T::kStep; i += T::kPer) {
         const int r = i + row;
         const bool valid = (mask >> r) & 1u;
         const int64_t kr = shfl64(ko, r), vr = shfl64(vo, r);
-        cp_async16(dst + T::at(r, vec), k + (valid ? kr + vec * 16 : 0), valid);
-        cp_async16(dst + T::kSide + T::at(r, vec), v + (valid ? vr + vec * 16 : 0), valid);
+        cp_async16(dst + T::at(r, vec), k + (valid ? kr : 0), valid);
+        cp_async16(dst + T::kSide + T::at(r, vec), v + (valid ? vr : 0), valid);
     }
 }
 
