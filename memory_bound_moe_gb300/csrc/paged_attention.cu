@@ -213,20 +213,21 @@ __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, in
 // Main kernel: NH groups of 8 query heads
 // ---------------------------------------------------------------------------
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NH>
 struct Tile {
-    static constexpr int kStepLog2 = E4M3 || D == 64 ? 5 : 4;
+    static constexpr int kStepLog2 = (E4M3 && D < 256) || D == 64 ? 5 : 4;
     static constexpr int kStep = 1 << kStepLog2;              // tokens of a warp's step
     static constexpr int kBytes = D * (E4M3 ? 1 : 2);         // of a token's head
     static constexpr int kVecs = kBytes / 16;
     static constexpr int kPer = kWarp / kVecs;                // rows that a warp copies with one instruction
     static constexpr int kSide = kStep * kBytes;              // keys or values of a step
     static constexpr int kStage = 2 * kSide;
-    static constexpr int kBlocks = D == 256 ? 1 : D == 128 && !E4M3 ? 2 : 3;   // of an SM
+    static constexpr int kBlocks = D == 256 ? (E4M3 ? 2 : 1) : D == 128 && (!E4M3 || NH == 2) ? 2 : 3;   // of an SM
     static constexpr int kStages = kBlocks == 3 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;            // of a warp
     static constexpr int kSmem = kWarps * kRing;
-    static_assert(kRows * D * 4 <= kStage, "a warp's output takes the place of a stage");
+    static constexpr int kRounds = NH * 8 * D * 4 <= kStage ? 1 : NH;   // a warp's output takes the place of a stage
+    static_assert(NH * 8 * D * 4 <= kStage * kRounds, "a stage holds a round's rows");
     // 16-byte vector v of row r lies at v ^ swz(r): 8 rows at the same vector hit 8 different banks of 16 bytes
     static __device__ __forceinline__ int swz(int r) { return kVecs >= 8 ? r & 7 : (r >> 1) & 3; }
     static __device__ __forceinline__ uint32_t at(int r, int v) { return uint32_t(r * kBytes + ((v ^ swz(r)) << 4)); }
@@ -240,10 +241,9 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
 
 // A step's keys and values into a stage. page: that of token t0 + lane %
 // kStep; mask: the tokens to be read, the others become zeros.
-template <int D, bool E4M3>
+template <typename T>
 __device__ __forceinline__ void load_step(uint32_t dst, const CacheView& c, const uint8_t* k, const uint8_t* v, int t0, int page,
                                           uint32_t mask) {
-    using T = Tile<D, E4M3>;
     const int lane = threadIdx.x % kWarp, vec = lane % T::kVecs, row = lane / T::kVecs;
     const int in_page = (1 << c.page_shift) - 1;
     constexpr uint32_t kAll = T::kStep == 32 ? 0xffffffffu : 0xffffu;
@@ -303,8 +303,8 @@ __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
 }
 
 template <int D, bool E4M3, int NH>
-__global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(const AttentionArgs a, int groups, int side, int ranks) {
-    using T = Tile<D, E4M3>;
+__global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_kernel(const AttentionArgs a, int groups, int side, int ranks) {
+    using T = Tile<D, E4M3, NH>;
     constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8, kStages = T::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_f[kWarps][kRows];
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
         if (kStep == 16) mask &= 0xffffu;
         if (more) {
             const int64_t head = ahead.unit / groups * side + mine_head;
-            load_step<D, E4M3>(ring_at + stage * T::kStage, a.cache, a.cache.k + head * a.cache.k_head,
+            load_step<T>(ring_at + stage * T::kStage, a.cache, a.cache.k + head * a.cache.k_head,
                                a.cache.v + head * a.cache.v_head, next_t0, next_page, mask);
         }
         cp_commit();
@@ -607,56 +607,66 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3>::kBlocks) attention_kernel(
                 s_m[warp][g + 8 * h] = m[h];
                 s_l[warp][g + 8 * h] = l[h];
             }
-#pragma unroll
-            for (int d = 0; d < kD16; ++d)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int col = E4M3 ? d * 16 + 2 * g + (z >> 1) : d * 16 + g + 8 * (z >> 1);
-                    mine[T::out_at(8 * h + 2 * quad + (z & 1), col)] = o[d][h][z];
-                }
         }
-        group_sync(mine_head, phases);
         const int seg = c.tiles();
         const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles, whole = begins && ends && ranks == 0;
         const int64_t slot = (2 * int64_t(blockIdx.x) + (begins ? 1 : 0)) * side + mine_head;
-        // what a warp's row counts in the sum of the head's warps, and for a whole unit in the output
-        for (int r = phase * kWarp + lane; r < rows; r += phases * kWarp) {
-            float most = -INFINITY, sum = 0.0f;
-            for (int w = mine_head; w < kWarps; w += side) most = fmaxf(most, s_m[w][r]);
-            const float base = most == -INFINITY ? 0.0f : most;
-            for (int w = mine_head; w < kWarps; w += side) sum += ex2_approx(s_m[w][r] - base) * s_l[w][r];
-            const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
-            for (int w = mine_head; w < kWarps; w += side) s_f[w][r] = ex2_approx(s_m[w][r] - base) * inv;
-            if (ranks > 0) {
-                s_cm[r] = most;
-                s_cl[r] = sum;
-            } else if (!whole) {
-                ws.m[slot * kRows + r] = most;
-                ws.l[slot * kRows + r] = sum;
-            } else if (a.lse != nullptr) {
-                a.lse[int64_t(c.b) * a.q_heads + h0 + r] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
+        constexpr int kHalf = NH / T::kRounds;   // groups of 8 rows of a round
+#pragma unroll
+        for (int h0r = 0; h0r < NH; h0r += kHalf) {
+#pragma unroll
+            for (int h = 0; h < kHalf; ++h)
+#pragma unroll
+                for (int d = 0; d < kD16; ++d)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int col = E4M3 ? d * 16 + 2 * g + (z >> 1) : d * 16 + g + 8 * (z >> 1);
+                        mine[T::out_at(8 * h + 2 * quad + (z & 1), col)] = o[d][h0r + h][z];
+                    }
+            group_sync(mine_head, phases);
+            if (h0r == 0) {
+                // what a warp's row counts in the sum of the head's warps, and for a whole unit in the output
+                for (int r = phase * kWarp + lane; r < rows; r += phases * kWarp) {
+                    float most = -INFINITY, sum = 0.0f;
+                    for (int w = mine_head; w < kWarps; w += side) most = fmaxf(most, s_m[w][r]);
+                    const float base = most == -INFINITY ? 0.0f : most;
+                    for (int w = mine_head; w < kWarps; w += side) sum += ex2_approx(s_m[w][r] - base) * s_l[w][r];
+                    const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+                    for (int w = mine_head; w < kWarps; w += side) s_f[w][r] = ex2_approx(s_m[w][r] - base) * inv;
+                    if (ranks > 0) {
+                        s_cm[r] = most;
+                        s_cl[r] = sum;
+                    } else if (!whole) {
+                        ws.m[slot * kRows + r] = most;
+                        ws.l[slot * kRows + r] = sum;
+                    } else if (a.lse != nullptr) {
+                        a.lse[int64_t(c.b) * a.q_heads + h0 + r] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
+                    }
+                }
+                group_sync(mine_head, phases);
             }
-        }
-        group_sync(mine_head, phases);
+            const int here = min(rows - 8 * h0r, 8 * kHalf);
 #pragma unroll 2
-        for (int i = phase * kWarp + lane; i < rows * (D / 4); i += phases * kWarp) {
-            const int r = i / (D / 4), d = i % (D / 4) * 4;
-            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int w = mine_head; w < kWarps; w += side) {
-                const float f = s_f[w][r];
-                const float4 z = *reinterpret_cast<const float4*>(s_out[w] + T::out_at(r, d));
-                y.x += f * z.x;
-                y.y += f * z.y;
-                y.z += f * z.z;
-                y.w += f * z.w;
+            for (int i = phase * kWarp + lane; i < here * (D / 4); i += phases * kWarp) {
+                const int r = 8 * h0r + i / (D / 4), d = i % (D / 4) * 4;
+                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int w = mine_head; w < kWarps; w += side) {
+                    const float f = s_f[w][r];
+                    const float4 z = *reinterpret_cast<const float4*>(s_out[w] + T::out_at(i / (D / 4), d));
+                    y.x += f * z.x;
+                    y.y += f * z.y;
+                    y.z += f * z.z;
+                    y.w += f * z.w;
+                }
+                if (ranks > 0)
+                    *reinterpret_cast<float4*>(s_co + r * D + d) = y;
+                else if (whole)
+                    *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
+                        make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+                else
+                    *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
             }
-            if (ranks > 0)
-                *reinterpret_cast<float4*>(s_co + r * D + d) = y;
-            else if (whole)
-                *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
-                    make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-            else
-                *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
+            if (h0r + kHalf < NH) group_sync(mine_head, phases);   // the next round's rows take the place of these
         }
         if (ranks == 0 && begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
         group_sync(mine_head, phases);   // the stages may be filled again
@@ -826,7 +836,7 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const Attention
 
 template <int D, bool E4M3, int NH>
 cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
-    using T = Tile<D, E4M3>;
+    using T = Tile<D, E4M3, NH>;
     static SmemGrant grant;
     auto kernel = attention_kernel<D, E4M3, NH>;
     cudaError_t err = grant.ensure(kernel);
