@@ -841,10 +841,12 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     auto kernel = attention_kernel<D, E4M3, NH>;
     cudaError_t err = grant.ensure(kernel);
     if (err != cudaSuccess) return err;
-    static const int occ = [&] {
+    const auto resident = [&](size_t smem) {
         int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNt, T::kSmem) == cudaSuccess && n > 0 ? n : 1;
-    }();
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNt, smem) == cudaSuccess && n > 0 ? n : 1;
+    };
+    constexpr int kShare = NH * 8 * D * 4;   // a block's share of a cluster's unit
+    static const int occ = resident(T::kSmem), cluster_occ = resident(T::kSmem + kShare);
     const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows;
     const int64_t table = int64_t(a.max_pages) << a.cache.page_shift, longest = a.window > 0 ? std::min<int64_t>(table, a.window) : table;
 
@@ -857,10 +859,9 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     // of keys per block, and fewer where few units leave most SMs idle.
     const int64_t clusters = int64_t(a.B) * a.cache.heads * groups;
     int ranks = kMaxRanks;
-    while (ranks > 0 && clusters * ranks * 8 > int64_t(num_sms) * occ * 7) ranks /= 2;
+    while (ranks > 0 && clusters * ranks * 8 > int64_t(num_sms) * cluster_occ * 7) ranks /= 2;
     if (ranks > 0 && longest * T::kBytes <= ranks * std::min<int64_t>(262144, 65536 + 16384 * clusters))
-        return launch_cluster(kernel, dim3(unsigned(clusters * ranks)), dim3(kNt), ranks, T::kSmem + unit_rows(group) * D * 4,
-                              stream, a, groups, 1, ranks);
+        return launch_cluster(kernel, dim3(unsigned(clusters * ranks)), dim3(kNt), ranks, T::kSmem + kShare, stream, a, groups, 1, ranks);
     const int side = heads_at_once(a.cache.heads);
     // no more blocks than the most tiles that these tables can hold need
     const int tile = kWarps / side * T::kStep;

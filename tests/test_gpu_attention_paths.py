@@ -1,0 +1,87 @@
+"""Paged attention where its ways of splitting the work meet: tables much wider
+than the sequences, units around the number of blocks, random calls."""
+from __future__ import annotations
+
+import random
+
+import pytest
+import torch
+
+from test_gpu_paged_attention import EDGES, KINDS, check, dev, make_cache, make_table, rng  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def widened(table, P, tokens):
+    """The same table with rows for `tokens` tokens; what lies behind the sequences is out of range."""
+    wide = torch.full((table.shape[0], max(table.shape[1], -(-tokens // P))), -9, dtype=torch.int32, device=table.device)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (16, 1), (6, 2), (9, 3), (32, 4), (64, 4), (20, 1)])
+def test_wide_tables(dev, kind, D, Hq, Hkv):  # noqa: F811
+    g = rng(dev, D + Hq)
+    lengths = EDGES + [1000, 3000]
+    table, pages = make_table(lengths, 16, dev, g)
+    cache, k, v = make_cache(pages, 16, Hkv, D, kind, dev, g)
+    q = torch.randn((len(lengths), Hq, D), generator=g, device=dev).to(torch.bfloat16)
+    n = torch.tensor(lengths, dtype=torch.int32, device=dev)
+    narrow = check(q, cache, k, v, table, n)
+    wide = check(q, cache, k, v, widened(table, 16, 200000), n)
+    for window in (1, 40, 999):
+        check(q, cache, k, v, table, n, window=window)
+    assert (narrow.float() - wide.float()).abs().max() <= 2.0 ** -6 * narrow.float().abs().max()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B", [1, 3, 32, 33, 34, 66, 67, 133, 134, 266, 267, 400])
+def test_units_around_the_number_of_blocks(dev, kind, B):  # noqa: F811
+    g = rng(dev, B)
+    lengths = [(37 * i) % 230 for i in range(B)]
+    table, pages = make_table(lengths, 8, dev, g)
+    cache, k, v = make_cache(pages, 8, 1, 128, kind, dev, g)
+    q = torch.randn((B, 5, 128), generator=g, device=dev).to(torch.bfloat16)
+    check(q, cache, k, v, table, torch.tensor(lengths, dtype=torch.int32, device=dev))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(dev, seed):  # noqa: F811
+    rnd = random.Random(seed)
+    g = rng(dev, seed)
+    Hkv, G, D, P = rnd.choice([1, 2, 3, 4, 5, 6, 8, 12]), rnd.choice([1, 2, 3, 5, 7, 8, 9, 12, 16, 18]), rnd.choice([64, 128, 256]), 2 ** rnd.randint(0, 8)
+    kind, layout = rnd.choice(KINDS), rnd.choice(["token", "head", "joint"])
+    B, top = rnd.choice([1, 2, 5, 17, 40]), rnd.choice([20, 300, 3000])
+    lengths = [rnd.randint(0, top) for _ in range(B)]
+    table, pages = make_table(lengths, P, dev, g)
+    if rnd.random() < 0.5:
+        table = widened(table, P, rnd.choice([1000, 20000, 300000]))
+    cache, k, v = make_cache(pages, P, Hkv, D, kind, dev, g, layout)
+    q = (rnd.choice([0.3, 1, 4]) * torch.randn((B, Hkv * G, D), generator=g, device=dev)).to(torch.bfloat16)
+    window = rnd.choice([0, 0, 0, rnd.randint(1, top)])
+    check(q, cache, k, v, table, torch.tensor(lengths, dtype=torch.int32, device=dev), window=window)
+
+
+def test_two_streams_with_their_own_workspaces(dev):  # noqa: F811
+    """Calls in flight at once give what they give alone."""
+    from memory_bound_moe_gb300 import moe_paged_attention, moe_paged_attention_workspace_size
+    g = rng(dev, 3)
+    jobs = []
+    for B, top, kind in ((3, 30000, "bf16"), (40, 900, "e4m3"), (2, 200, "bf16")):
+        lengths = [top - 7 * i for i in range(B)]
+        table, pages = make_table(lengths, 16, dev, g)
+        cache, k, v = make_cache(pages, 16, 4, 128, kind, dev, g)
+        q = torch.randn((B, 32, 128), generator=g, device=dev).to(torch.bfloat16)
+        n = torch.tensor(lengths, dtype=torch.int32, device=dev)
+        ws = torch.empty(moe_paged_attention_workspace_size(B, 32, 4, 128), dtype=torch.uint8, device=dev)
+        jobs.append((q, cache, table, n, ws, torch.empty_like(q), torch.cuda.Stream()))
+    alone = [moe_paged_attention(q, c, t, n, workspace=ws).clone() for q, c, t, n, ws, _, _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for q, c, t, n, ws, out, s in jobs:
+            moe_paged_attention(q, c, t, n, workspace=ws, out=out, stream=s)
+    torch.cuda.synchronize()
+    for (_, _, _, _, _, out, _), want in zip(jobs, alone):
+        assert torch.equal(out, want)
