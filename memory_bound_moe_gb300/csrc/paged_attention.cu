@@ -223,7 +223,7 @@ struct Tile {
     static constexpr int kSide = kStep * kBytes;              // keys or values of a step
     static constexpr int kStage = 2 * kSide;
     static constexpr int kBlocks = D == 256 ? (E4M3 ? 2 : 1) : D == 128 && (!E4M3 || NH == 2) ? 2 : 3;   // of an SM
-    static constexpr int kStages = kBlocks == 3 ? 2 : 3;
+    static constexpr int kStages = kBlocks < 3 || kStage == 4096 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;            // of a warp
     static constexpr int kSmem = kWarps * kRing;
     static constexpr int kRounds = NH * 8 * D * 4 <= kStage ? 1 : NH;   // a warp's output takes the place of a stage
