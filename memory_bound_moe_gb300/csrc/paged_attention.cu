@@ -158,6 +158,11 @@ struct Cursor {
     }
 };
 
+// a / b of non-negative numbers: a 64-bit division takes four times as long.
+__device__ __forceinline__ int64_t divide(int64_t a, uint32_t b) {
+    return a >> 32 == 0 ? int64_t(uint32_t(a) / b) : a / b;
+}
+
 // This block's run. Every block adds up the sequences' tiles for itself. A
 // thread's sequences are a run of them, so that the thread in whose range this
 // block's run begins can walk to its sequence. `run`: tiles of a run.
@@ -185,7 +190,7 @@ __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, in
         if (w < warp) before += s_warp[w];
         total += s_warp[w];
     }
-    run = max(int64_t(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
+    run = max(int64_t(kMinTiles), divide(total + gridDim.x - 1, gridDim.x));
     const int64_t start = run * blockIdx.x;
     if (before <= start && start < before + sum) {
         int b = b0;
@@ -203,8 +208,8 @@ __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, in
     if (c.left > 0) {
         c.b = s_b;
         c.s = span_of(a, c.b, ts);
-        c.unit = int((start - s_base) / c.s.tiles);
-        c.local = int((start - s_base) % c.s.tiles);
+        c.unit = int(divide(start - s_base, c.s.tiles));
+        c.local = int(start - s_base - int64_t(c.unit) * c.s.tiles);
     }
     return c;
 }
@@ -353,13 +358,20 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
     Cursor ahead = c;
     int ahead_from = 0, ahead_j = 0, ahead_steps = 0, next_t0 = 0, next_page = -1;
     bool more = c.left > 0;
-    if (more) ahead_steps = open(ahead, ahead_from);
+    const uint8_t *ahead_k = nullptr, *ahead_v = nullptr;   // of the unit's head
+    const auto enter = [&]() {
+        const int64_t head = ahead.unit / groups * side + mine_head;
+        ahead_k = a.cache.k + head * a.cache.k_head;
+        ahead_v = a.cache.v + head * a.cache.v_head;
+        ahead_steps = open(ahead, ahead_from);
+    };
+    if (more) enter();
     const auto look = [&]() {
         while (more && ahead_j >= ahead_steps) {
             ahead.next_unit(a, units, ts);
             more = ahead.left > 0;
             ahead_j = 0;
-            if (more) ahead_steps = open(ahead, ahead_from);
+            if (more) enter();
         }
         next_page = -1;
         if (more) {
@@ -374,11 +386,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
     const auto issue = [&](int stage) -> uint32_t {
         uint32_t mask = __ballot_sync(kFull, next_page >= 0);
         if (kStep == 16) mask &= 0xffffu;
-        if (more) {
-            const int64_t head = ahead.unit / groups * side + mine_head;
-            load_step<T>(ring_at + stage * T::kStage, a.cache, a.cache.k + head * a.cache.k_head,
-                               a.cache.v + head * a.cache.v_head, next_t0, next_page, mask);
-        }
+        if (more) load_step<T>(ring_at + stage * T::kStage, a.cache, ahead_k, ahead_v, next_t0, next_page, mask);
         cp_commit();
         look();
         return mask;
