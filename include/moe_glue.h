@@ -493,7 +493,9 @@ moe_status_t moe_layer_fp4(const float* logits, int64_t T, int E, int k, int ren
  * keys is k[page * k_page_stride + token * k_token_stride + head * k_head_stride
  * + d]; the values likewise. Any non-negative strides (in elements) that are
  * whole 16-byte vectors will do, so pages may hold tokens of all heads or heads
- * of all tokens, and k and v may be interleaved views of one array. Elements
+ * of all tokens, and k and v may be interleaved views of one array (without a
+ * common element). In the checks for overlaps a cache is the whole address range
+ * from its first to its last element. Elements
  * are bfloat16 (MOE_KV_BF16) or E4M3 bytes (MOE_KV_E4M3) that stand for E4M3 *
  * k_scale or E4M3 * v_scale. The struct is read during the call; k and v are
  * device pointers, 16-byte aligned (MOE_ERR_MISALIGNED).

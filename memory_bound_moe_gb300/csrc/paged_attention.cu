@@ -7,20 +7,34 @@
 // cache bounds it, and mma.sync keeps up with HBM at a quarter of its rate; a
 // 128-row tcgen05 tile would be empty to seven eighths or more.
 //
-// Split. A unit of work is (sequence, key heads side by side, group of 16 heads). All units'
-// tiles, one after another, are cut into equal runs, one per resident block:
-// whatever the lengths are, every SM reads the same number of bytes (the
-// lengths are on the GPU, so every block adds them up for itself). A unit
-// inside one run is finished there; what a run has of a unit that goes on in
-// another run goes to the workspace (at most two per run), and a second kernel
-// joins those in order of the runs.
+// Split. A unit of work is (sequence, key heads side by side, group of 16
+// heads). All units' tiles, one after another, are cut into equal runs, one per
+// resident block: whatever the lengths are, every SM reads the same number of
+// bytes (the lengths are on the GPU, so every block adds them up for itself). A
+// unit inside one run is finished there; what a run has of a unit that goes on
+// in another run goes to the workspace (at most two per run), and a second
+// kernel joins those in order of the runs. Units that are few and short go to a
+// cluster of blocks each instead, which joins them in its shared memory.
 //
-// A block's 4 warps read up to 4 key heads of the same tokens, or steps (16 or 32
-// tokens) in turn of fewer heads, and never meet inside a unit: each has its own ring of kStages steps in shared memory, filled
-// by 16-byte cp.async, and its own running maximum, sum and output (online
-// softmax); warps of the same head are joined when the run leaves the unit. The ring goes on
-// over the units: the next ones' first steps are on their way while one is
-// finished, in the stage that was read last.
+// A block's 4 warps read up to 4 key heads of the same tokens, or steps (16 or
+// 32 tokens) in turn of fewer heads, and never meet inside a unit: each has its
+// own ring of kStages steps in shared memory, filled by 16-byte cp.async, and
+// its own running maximum, sum and output (online softmax); warps of the same
+// head are joined when the run leaves the unit. The ring goes on over the units:
+// the next ones' first steps are on their way while one is finished, in the
+// stage that was read last.
+//
+// The output is held transposed, 16 columns as a product's rows and 8 heads as
+// its columns: the weights leave the scores' product in just the layout that the
+// next one takes them in, up to 8 heads need half the products, and the values
+// come through ldmatrix.trans.
+//
+// Measured on GB300 (6.77 TB/s copy): 1.07 GB of keys and values at 6.5 TB/s (two
+// sequences of 131072 tokens), 6.3 (256 of up to 4096), 6.1 (8 bits); 394 MB at
+// 5.7. DRAM is 70% busy in 270 MB, the warps issue 27% of the time (45% with 8
+// bits, whose conversions take the ALU pipe to 43%). Runs cost 12 us beside the
+// reading: 4 to the first step's arrival, 3 as SMs differ in speed, 2 to leave
+// the last unit, 4 for the second kernel.
 #include "few_device.cuh"
 #include "moe_launch.h"
 
@@ -227,7 +241,11 @@ struct Tile {
     static constexpr int kPer = kWarp / kVecs;                // rows that a warp copies with one instruction
     static constexpr int kSide = kStep * kBytes;              // keys or values of a step
     static constexpr int kStage = 2 * kSide;
-    static constexpr int kBlocks = D == 256 ? (E4M3 ? 2 : 1) : D == 128 && (!E4M3 || NH == 2) ? 2 : 3;   // of an SM
+    // Of an SM; the rings fill its shared memory, and the registers allow no more. 394 MB, 8 heads a
+    // key head: bfloat16 heads of 128 68.6 us with 2 blocks of 3 stages, 256 ragged sequences of it
+    // 171 us (3 blocks of 2 stages 179 us); 8-bit heads of 64 77.2 us with 3 blocks of 3 stages, 79.2
+    // with 4, 83.3 with 3 of 2.
+    static constexpr int kBlocks = D == 256 ? (E4M3 ? 2 : 1) : D == 128 && (!E4M3 || NH == 2) ? 2 : 3;
     static constexpr int kStages = kBlocks < 3 || kStage == 4096 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;            // of a warp
     static constexpr int kSmem = kWarps * kRing;
@@ -697,6 +715,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
 #pragma unroll
         for (int k = 0; k < kMaxRanks; ++k) {
             m1[k] = -INFINITY;
+            l1[k] = 0.0f;
             if (k < ranks) {
                 m1[k] = ld_cluster(s_cm + r, k);
                 l1[k] = ld_cluster(s_cl + r, k);
@@ -710,7 +729,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
         float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < kMaxRanks; ++k)
-            if (m1[k] != -INFINITY) {   // a block without tokens left nothing
+            if (l1[k] != 0.0f) {   // a block without tokens left no output
                 const float f = ex2_approx(m1[k] - base);
                 sum += f * l1[k];
                 y.x += f * z[k].x;

@@ -85,3 +85,23 @@ def test_two_streams_with_their_own_workspaces(dev):  # noqa: F811
     torch.cuda.synchronize()
     for (_, _, _, _, _, out, _), want in zip(jobs, alone):
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_keys_that_are_not_numbers(dev, kind, wide):  # noqa: F811
+    """A run of NaN keys, whoever reads it, makes its sequence's results NaN and no other's."""
+    from memory_bound_moe_gb300 import moe_paged_attention
+    g = rng(dev, 4)
+    lengths = [700, 700, 700, 64, 20]
+    table, pages = make_table(lengths, 16, dev, g)
+    cache, k, v = make_cache(pages, 16, 1, 128, kind, dev, g)
+    bits = k.view(torch.int16) if kind == "bf16" else k.view(torch.uint8)
+    for b, (lo, hi) in enumerate(((0, 192), (512, 700), (0, 0), (0, 64), (0, 0))):
+        for page in range(lo // 16, -(-hi // 16)):
+            bits[int(table[b, page])] = 0x7fc0 if kind == "bf16" else 0x7f
+    q = torch.randn((5, 4, 128), generator=g, device=dev).to(torch.bfloat16)
+    if wide:
+        table = widened(table, 16, 200000)
+    out = moe_paged_attention(q, cache, table, torch.tensor(lengths, dtype=torch.int32, device=dev))
+    assert out[[0, 1, 3]].isnan().all() and out[[2, 4]].isfinite().all()
