@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
             }
             // Weights 2^(x - m). As f16 (E4M3) they are times 2^15, so that those down to 2^-39 of the
             // largest count. As bfloat16 they are two terms, the upper half of the float and what it
-            // leaves (one alone would cost as much as the output's own rounding); the second is never 0,
-            // so that an infinite value does not become NaN by it.
+            // leaves (one alone would cost as much as the output's own rounding); the second is never 0
+            // but at least 2^-20 of the weight, so that an infinite value does not become NaN by it.
             uint32_t p[NH][kTiles8], lo[NH][kTiles8];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
                         p[h][n] = pack_f16x2(p0, p1);
                     } else {
                         p[h][n] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-                        lo[h][n] = pack_bf16x2(fmaxf(p0 - bf16_lo(p[h][n]), 1.2e-38f), fmaxf(p1 - bf16_hi(p[h][n]), 1.2e-38f));
+                        lo[h][n] = pack_bf16x2(fmaxf(p0 - bf16_lo(p[h][n]), p0 * 0x1p-20f), fmaxf(p1 - bf16_hi(p[h][n]), p1 * 0x1p-20f));
                     }
                 }
             }

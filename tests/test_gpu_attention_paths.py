@@ -105,3 +105,21 @@ def test_many_keys_that_are_not_numbers(dev, kind, wide):  # noqa: F811
         table = widened(table, 16, 200000)
     out = moe_paged_attention(q, cache, table, torch.tensor(lengths, dtype=torch.int32, device=dev))
     assert out[[0, 1, 3]].isnan().all() and out[[2, 4]].isfinite().all()
+
+
+def test_values_of_very_different_size(dev):  # noqa: F811
+    """Values near the largest bfloat16 at tokens whose weights vanish."""
+    g = rng(dev, 6)
+    lengths = [400, 33]
+    table, pages = make_table(lengths, 16, dev, g)
+    cache, k, v = make_cache(pages, 16, 1, 64, "bf16", dev, g)
+    q = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device=dev)
+    q[..., 0] = 1.0
+    # scores 0 for one token in eight, far below that for the others: weights of e^-60 to e^-400
+    far = torch.arange(400, device=dev) % 8
+    for b, n in enumerate(lengths):
+        at = torch.arange(n, device=dev)
+        page = table[b].long()[at // 16]
+        k[page, at % 16, 0, 0] = -(far[:n] * 57 + (far[:n] > 0) * 3).to(torch.bfloat16)
+        v[page, at % 16, 0, 1] = torch.where(far[:n] > 1, 3e38, 1.0).to(torch.bfloat16)
+    check(q, cache, k, v, table, torch.tensor(lengths, dtype=torch.int32, device=dev), scale=1.0)
