@@ -426,41 +426,45 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
 
     Note note = {-1, 0, 0, 0};
     int64_t pos = run * blockIdx.x;
+    // q, as A: row g (and g + 8) is head h0 + g. For E4M3 the order of the 16 columns of a product is
+    // that in which the keys' bytes come out of ldmatrix: 4 quad .. 4 quad + 3.
+    uint32_t aq[kD16][4];
+    const auto load_q = [&](const Cursor& p) {
+        const int chunk = p.unit % groups, rows = min(kRows, group - chunk * kRows);
+        const int h0 = (p.unit / groups * side + mine_head) * group + chunk * kRows;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h;
+            const uint16_t* q = a.q + int64_t(p.b) * a.q_stride + int64_t(h0 + r) * D;
+#pragma unroll
+            for (int k = 0; k < kD16; ++k) {
+                if constexpr (!E4M3) {
+                    aq[k][h] = h < NH && r < rows ? *reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2) : 0u;
+                    aq[k][h + 2] = h < NH && r < rows ? *reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2 + 8) : 0u;
+                } else {
+                    const uint2 w = h < NH && r < rows ? *reinterpret_cast<const uint2*>(q + k * 16 + quad * 4) : make_uint2(0u, 0u);
+                    aq[k][h] = w.x;
+                    aq[k][h + 2] = w.y;
+                }
+            }
+        }
+    };
+    if (c.left > 0) load_q(c);
     while (c.left > 0) {
         const int head = c.unit / groups * side + mine_head, chunk = c.unit % groups;
         const int rows = min(kRows, group - chunk * kRows);
         const int h0 = head * group + chunk * kRows;
 
-        // q, as A: row g (and g + 8) is head h0 + g. For E4M3 the order of the 16 columns of a
-        // product is that in which the keys' bytes come out of ldmatrix: 4 quad .. 4 quad + 3.
-        uint32_t aq[kD16][4];
         float f_row[NH];   // what a row's scores are multiplied by, with log2 e
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (h >= NH) {
-#pragma unroll
-                for (int k = 0; k < kD16; ++k) aq[k][h] = aq[k][h + 2] = 0u;
-                continue;
-            }
-            const int r = g + 8 * h;
-            const uint16_t* q = a.q + int64_t(c.b) * a.q_stride + int64_t(h0 + r) * D;
+        for (int h = 0; h < NH; ++h) {
             f_row[h] = a.scale * a.cache.k_scale * kLog2e;
-            if constexpr (!E4M3) {
-#pragma unroll
-                for (int k = 0; k < kD16; ++k) {
-                    aq[k][h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2) : 0u;
-                    aq[k][h + 2] = r < rows ? *reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2 + 8) : 0u;
-                }
-            } else {
+            if constexpr (E4M3) {
                 float most = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kD16; ++k) {
-                    const uint2 w = r < rows ? *reinterpret_cast<const uint2*>(q + k * 16 + quad * 4) : make_uint2(0u, 0u);
-                    aq[k][h] = w.x;
-                    aq[k][h + 2] = w.y;
-                    most = fmaxf(fmaxf(most, fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x)))),
-                                 fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y))));
-                }
+                for (int k = 0; k < kD16; ++k)
+#pragma unroll
+                    for (int z = h; z < 4; z += 2) most = fmaxf(most, fmaxf(fabsf(bf16_lo(aq[k][z])), fabsf(bf16_hi(aq[k][z]))));
                 most = fmaxf(most, __shfl_xor_sync(kFull, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(kFull, most, 2));
                 // f16 holds q times 2^(14 - e), e the exponent of the row's largest (1 for a row of zeros or with an infinity)
@@ -468,10 +472,9 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
                 const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
                 f_row[h] *= __uint_as_float(uint32_t(127 - 14 + e) << 23);
 #pragma unroll
-                for (int k = 0; k < kD16; ++k) {
-                    aq[k][h] = pack_f16x2(bf16_lo(aq[k][h]) * up, bf16_hi(aq[k][h]) * up);
-                    aq[k][h + 2] = pack_f16x2(bf16_lo(aq[k][h + 2]) * up, bf16_hi(aq[k][h + 2]) * up);
-                }
+                for (int k = 0; k < kD16; ++k)
+#pragma unroll
+                    for (int z = h; z < 4; z += 2) aq[k][z] = pack_f16x2(bf16_lo(aq[k][z]) * up, bf16_hi(aq[k][z]) * up);
             }
         }
 
@@ -621,6 +624,11 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
             }
         }
 
+        // the next unit's q, on its way while this one is finished
+        Cursor next = c;
+        next.next_unit(a, units, ts);
+        if (next.left > 0) load_q(next);
+
         // this warp's result into the stage that no load is on its way to
         __syncwarp();
         float* const mine = reinterpret_cast<float*>(ring + (stage == 0 ? kStages - 1 : stage - 1) * T::kStage);
@@ -697,7 +705,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
         if (ranks == 0 && begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
         group_sync(mine_head, phases);   // the stages may be filled again
         pos += seg;
-        c.next_unit(a, units, ts);
+        c = next;
     }
     if (ranks == 0) {
         if (threadIdx.x == 0) ws.notes[blockIdx.x] = note;
