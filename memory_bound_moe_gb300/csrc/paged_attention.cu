@@ -45,7 +45,11 @@ constexpr int kWarps = 4;
 constexpr int kNt = kWarps * kWarp;
 constexpr int kRows = 16;            // query heads of a unit, at most
 constexpr int kMaxBlocks = 640;      // runs the workspace holds the ends of
-constexpr int kMinTiles = 2;         // tiles of a run, at least
+constexpr int kMinTiles = 3;         // tiles of a run, at least
+// Tiles that entering and leaving a unit counts in a run: about 2 us, in which a warp's ring runs dry
+// (GB300, the decode batch of 16 sequences of 1 to 8192 tokens: 53.9 us at 0, 52.4 at 1, 52.2 at 2).
+constexpr int kUnitCost = 2;
+static_assert(kMinTiles > kUnitCost, "a run goes on");
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // ---------------------------------------------------------------------------
@@ -154,8 +158,8 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b, int ts) {
     return s;
 }
 
-// A place in a run: `left` tiles of it from tile `local` of unit `unit` of
-// sequence b on.
+// A place in a run: it goes on with `left` tiles (and the cost of other units)
+// from tile `local` of unit `unit` of sequence b on.
 struct Cursor {
     int64_t left;
     int b, unit, local;
@@ -164,6 +168,7 @@ struct Cursor {
     __device__ __forceinline__ void next_unit(const AttentionArgs& a, int units, int ts) {
         left -= tiles();
         local = 0;
+        left = max(int64_t(0), left - kUnitCost);
         if (++unit == units && left > 0) {
             unit = 0;
             do s = span_of(a, ++b, ts);
@@ -179,15 +184,20 @@ __device__ __forceinline__ int64_t divide(int64_t a, uint32_t b) {
 
 // This block's run. Every block adds up the sequences' tiles for itself. A
 // thread's sequences are a run of them, so that the thread in whose range this
-// block's run begins can walk to its sequence. `run`: tiles of a run.
+// block's run begins can walk to its sequence. A unit counts its tiles and, in
+// front of them, kUnitCost. `run`: the length of a run.
 __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, int ts, int64_t& run) {
     __shared__ int64_t s_warp[kWarps];
     __shared__ int64_t s_base;
     __shared__ int s_b;
     const int per = (a.B + kNt - 1) / kNt, b0 = min(a.B, int(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    const auto count = [&](int b) {
+        const int tiles = span_of(a, b, ts).tiles;
+        return tiles > 0 ? tiles + kUnitCost : 0;
+    };
     int64_t sum = 0;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) sum += span_of(a, b, ts).tiles;
+    for (int b = b0; b < b1; ++b) sum += count(b);
     sum *= units;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     int64_t x = sum;
@@ -208,10 +218,10 @@ __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, in
     const int64_t start = run * blockIdx.x;
     if (before <= start && start < before + sum) {
         int b = b0;
-        int64_t n = int64_t(span_of(a, b, ts).tiles) * units;
+        int64_t n = int64_t(count(b)) * units;
         while (before + n <= start) {
             before += n;
-            n = int64_t(span_of(a, ++b, ts).tiles) * units;
+            n = int64_t(count(++b)) * units;
         }
         s_base = before;
         s_b = b;
@@ -222,8 +232,11 @@ __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, in
     if (c.left > 0) {
         c.b = s_b;
         c.s = span_of(a, c.b, ts);
-        c.unit = int(divide(start - s_base, c.s.tiles));
-        c.local = int(start - s_base - int64_t(c.unit) * c.s.tiles);
+        const int n = c.s.tiles + kUnitCost;
+        c.unit = int(divide(start - s_base, n));
+        const int at = int(start - s_base - int64_t(c.unit) * n);
+        c.local = max(0, at - kUnitCost);
+        c.left = max(int64_t(0), c.left - max(0, kUnitCost - at));
     }
     return c;
 }
@@ -425,7 +438,6 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
         }
 
     Note note = {-1, 0, 0, 0};
-    int64_t pos = run * blockIdx.x;
     // q, as A: row g (and g + 8) is head h0 + g. For E4M3 the order of the 16 columns of a product is
     // that in which the keys' bytes come out of ldmatrix: 4 quad .. 4 quad + 3.
     uint32_t aq[kD16][4];
@@ -702,9 +714,11 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
             }
             if (h0r + kHalf < NH) group_sync(mine_head, phases);   // the next round's rows take the place of these
         }
-        if (ranks == 0 && begins && !ends) note = {c.b, c.unit, int((pos + c.s.tiles - 1) / run), int(blockIdx.x)};
+        if (ranks == 0 && begins && !ends) {   // what is left of the unit fills the next runs
+            const int rest = c.s.tiles - seg, more_runs = rest <= run ? 1 : (rest + int(run) - 1) / int(run);
+            note = {c.b, c.unit, int(blockIdx.x) + more_runs, int(blockIdx.x)};
+        }
         group_sync(mine_head, phases);   // the stages may be filled again
-        pos += seg;
         c = next;
     }
     if (ranks == 0) {
@@ -900,7 +914,7 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     const int side = heads_at_once(a.cache.heads);
     // no more blocks than the most tiles that these tables can hold need
     const int tile = kWarps / side * T::kStep;
-    const int64_t tiles = (longest + tile - 1) / tile + 1;
+    const int64_t tiles = (longest + tile - 1) / tile + 1 + kUnitCost;
     const int64_t most = (tiles * (a.cache.heads / side) * groups * a.B + kMinTiles - 1) / kMinTiles;
     const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, most})));
     err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups, side, 0);
