@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
         for (int h = 0; h < NH; ++h) {
             l[h] += __shfl_xor_sync(kFull, l[h], 1);
             l[h] += __shfl_xor_sync(kFull, l[h], 2);
-            if (quad == 0) {
+            if (quad == 0 && phases > 1) {
                 s_m[warp][g + 8 * h] = m[h];
                 s_l[warp][g + 8 * h] = l[h];
             }
@@ -657,6 +657,24 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
         const int seg = c.tiles();
         const bool begins = c.local == 0, ends = c.local + seg == c.s.tiles, whole = begins && ends && ranks == 0;
         const int64_t slot = (2 * int64_t(blockIdx.x) + (begins ? 1 : 0)) * side + mine_head;
+        // a row's largest score and sum, where they are the whole unit's: log-sum-exp; else into the workspace
+        const auto store_sum = [&](int r, float most, float sum) {
+            if (!whole) {
+                ws.m[slot * kRows + r] = most;
+                ws.l[slot * kRows + r] = sum;
+            } else if (a.lse != nullptr) {
+                a.lse[int64_t(c.b) * a.q_heads + h0 + r] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
+            }
+        };
+        const auto store_row = [&](int r, int d, const float4& y) {
+            if (ranks > 0)
+                *reinterpret_cast<float4*>(s_co + r * D + d) = y;
+            else if (whole)
+                *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
+                    make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            else
+                *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
+        };
         constexpr int kHalf = NH / T::kRounds;   // groups of 8 rows of a round
 #pragma unroll
         for (int h0r = 0; h0r < NH; h0r += kHalf) {
@@ -669,6 +687,34 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
                         const int col = E4M3 ? d * 16 + 2 * g + (z >> 1) : d * 16 + g + 8 * (z >> 1);
                         mine[T::out_at(8 * h + 2 * quad + (z & 1), col)] = o[d][h0r + h][z];
                     }
+            const int here = min(rows - 8 * h0r, 8 * kHalf), pieces = here * (D / 4);
+            if (phases == 1) {   // a warp has the head to itself
+                float f[kHalf];
+#pragma unroll
+                for (int h = 0; h < kHalf; ++h) {
+                    const float sum = l[h0r + h];
+                    f[h] = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+                    if (quad == 0 && g + 8 * (h0r + h) < rows) store_sum(g + 8 * (h0r + h), m[h0r + h], sum);
+                }
+                __syncwarp();
+                for (int i = lane; i - lane < pieces; i += kWarp) {
+                    const int r = i / (D / 4), d = i % (D / 4) * 4;
+                    float factor = __shfl_sync(kFull, f[0], r % 8 * 4);
+                    if (kHalf == 2) {
+                        const float other = __shfl_sync(kFull, f[kHalf - 1], r % 8 * 4);
+                        factor = r < 8 ? factor : other;
+                    }
+                    if (i >= pieces) continue;
+                    float4 y = *reinterpret_cast<const float4*>(mine + T::out_at(r, d));
+                    y.x *= factor;
+                    y.y *= factor;
+                    y.z *= factor;
+                    y.w *= factor;
+                    store_row(8 * h0r + r, d, y);
+                }
+                __syncwarp();   // the next round, or the next loads, take the place of these rows
+                continue;
+            }
             group_sync(mine_head, phases);
             if (h0r == 0) {
                 // what a warp's row counts in the sum of the head's warps, and for a whole unit in the output
@@ -682,18 +728,14 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
                     if (ranks > 0) {
                         s_cm[r] = most;
                         s_cl[r] = sum;
-                    } else if (!whole) {
-                        ws.m[slot * kRows + r] = most;
-                        ws.l[slot * kRows + r] = sum;
-                    } else if (a.lse != nullptr) {
-                        a.lse[int64_t(c.b) * a.q_heads + h0 + r] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
+                    } else {
+                        store_sum(r, most, sum);
                     }
                 }
                 group_sync(mine_head, phases);
             }
-            const int here = min(rows - 8 * h0r, 8 * kHalf);
 #pragma unroll 2
-            for (int i = phase * kWarp + lane; i < here * (D / 4); i += phases * kWarp) {
+            for (int i = phase * kWarp + lane; i < pieces; i += phases * kWarp) {
                 const int r = 8 * h0r + i / (D / 4), d = i % (D / 4) * 4;
                 float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int w = mine_head; w < kWarps; w += side) {
@@ -704,13 +746,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
                     y.z += f * z.z;
                     y.w += f * z.w;
                 }
-                if (ranks > 0)
-                    *reinterpret_cast<float4*>(s_co + r * D + d) = y;
-                else if (whole)
-                    *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
-                        make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-                else
-                    *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
+                store_row(r, d, y);
             }
             if (h0r + kHalf < NH) group_sync(mine_head, phases);   // the next round's rows take the place of these
         }
@@ -718,7 +754,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
             const int rest = c.s.tiles - seg, more_runs = rest <= run ? 1 : (rest + int(run) - 1) / int(run);
             note = {c.b, c.unit, int(blockIdx.x) + more_runs, int(blockIdx.x)};
         }
-        group_sync(mine_head, phases);   // the stages may be filled again
+        if (phases > 1) group_sync(mine_head, phases);   // the stages may be filled again
         c = next;
     }
     if (ranks == 0) {
