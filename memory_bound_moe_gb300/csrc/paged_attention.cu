@@ -7,8 +7,8 @@
 // cache bounds it, and mma.sync keeps up with HBM at a quarter of its rate; a
 // 128-row tcgen05 tile would be empty to seven eighths or more.
 //
-// Split. A unit of work is (sequence, key heads side by side, group of 16
-// heads). All units' tiles, one after another, are cut into equal runs, one per
+// Split. A unit of work is (sequence, up to 4 key heads, or groups of 16 query
+// heads of one, side by side). All units' tiles, one after another, are cut into equal runs, one per
 // resident block: whatever the lengths are, every SM reads the same number of
 // bytes (the lengths are on the GPU, so every block adds them up for itself). A
 // unit inside one run is finished there; what a run has of a unit that goes on
@@ -69,10 +69,11 @@ struct Partials {
     Note* notes;   // [blocks]
 };
 
-// Key heads that a block's warps read side by side: a token's heads lie beside
-// each other in most caches, so its bytes are asked for together, and warps of
-// different heads have nothing to join.
-inline int heads_at_once(int heads) { return heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1; }
+// Key heads (or groups of 16 query heads of one) that a block's warps read side
+// by side: a token's heads lie beside each other in most caches, so its bytes
+// are asked for together, groups of a head find theirs in L2, and such warps have
+// nothing to join. all: key heads times groups.
+inline int heads_at_once(int all) { return all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1; }
 
 __host__ __device__ inline int unit_rows(int group) { return group < kRows ? group : kRows; }
 
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
     __shared__ float s_cm[kRows], s_cl[kRows];   // this block's share of a cluster's unit
     pdl_wait_and_release();
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, g = lane / 4, quad = lane % 4;
-    const int heads = a.cache.heads, group = a.q_heads / heads, units = heads / side * groups;
+    const int heads = a.cache.heads, group = a.q_heads / heads, units = heads * groups / side;
     const int mine_head = warp % side, phase = warp / side, phases = kWarps / side;
     const int ts = __ffs(kStep * phases) - 1;
     const Partials ws = partials(a.workspace, gridDim.x * side, unit_rows(group), D);
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
     bool more = c.left > 0;
     const uint8_t *ahead_k = nullptr, *ahead_v = nullptr;   // of the unit's head
     const auto enter = [&]() {
-        const int64_t head = ahead.unit / groups * side + mine_head;
+        const int64_t head = (ahead.unit * side + mine_head) / groups;
         ahead_k = a.cache.k + head * a.cache.k_head;
         ahead_v = a.cache.v + head * a.cache.v_head;
         ahead_steps = open(ahead, ahead_from);
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
     // that in which the keys' bytes come out of ldmatrix: 4 quad .. 4 quad + 3.
     uint32_t aq[kD16][4];
     const auto load_q = [&](const Cursor& p) {
-        const int chunk = p.unit % groups, rows = min(kRows, group - chunk * kRows);
-        const int h0 = (p.unit / groups * side + mine_head) * group + chunk * kRows;
+        const int at = p.unit * side + mine_head, chunk = at % groups, rows = min(kRows, group - chunk * kRows);
+        const int h0 = at / groups * group + chunk * kRows;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = g + 8 * h;
@@ -463,9 +464,8 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_ker
     };
     if (c.left > 0) load_q(c);
     while (c.left > 0) {
-        const int head = c.unit / groups * side + mine_head, chunk = c.unit % groups;
-        const int rows = min(kRows, group - chunk * kRows);
-        const int h0 = head * group + chunk * kRows;
+        const int at = c.unit * side + mine_head, chunk = at % groups;
+        const int rows = min(kRows, group - chunk * kRows), h0 = at / groups * group + chunk * kRows;
 
         float f_row[NH];   // what a row's scores are multiplied by, with log2 e
 #pragma unroll
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const Attention
     const int r = item % urows, side_head = item % rows_all / urows;
     const bool in = item < units * rows_all;
     const Note n = in ? s_note[item / rows_all] : Note{};
-    const int chunk = n.unit % groups, head = n.unit / groups * side + side_head;
+    const int chunk = (n.unit * side + side_head) % groups, head = (n.unit * side + side_head) / groups;
     const bool valid = in && r < group - chunk * kRows;   // the last group of 16 may be smaller
     const int parts = valid ? n.last - n.run + 1 : 0;
     float m = -INFINITY, l = 0.0f;
@@ -947,17 +947,17 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     while (ranks > 0 && clusters * ranks * 8 > int64_t(num_sms) * cluster_occ * 7) ranks /= 2;
     if (ranks > 0 && longest * T::kBytes <= ranks * std::min<int64_t>(262144, 65536 + 16384 * clusters))
         return launch_cluster(kernel, dim3(unsigned(clusters * ranks)), dim3(kNt), ranks, T::kSmem + kShare, stream, a, groups, 1, ranks);
-    const int side = heads_at_once(a.cache.heads);
+    const int side = heads_at_once(a.cache.heads * groups);
     // no more blocks than the most tiles that these tables can hold need
     const int tile = kWarps / side * T::kStep;
     const int64_t tiles = (longest + tile - 1) / tile + 1 + kUnitCost;
-    const int64_t most = (tiles * (a.cache.heads / side) * groups * a.B + kMinTiles - 1) / kMinTiles;
+    const int64_t most = (tiles * (a.cache.heads * groups / side) * a.B + kMinTiles - 1) / kMinTiles;
     const int blocks = int(std::max<int64_t>(1, std::min<int64_t>({int64_t(num_sms) * occ, kMaxBlocks, most})));
     err = launch_pdl(kernel, dim3(blocks), dim3(kNt), T::kSmem, stream, a, groups, side, 0);
     if (err != cudaSuccess) return err;
     // Units that may be split: all of them, or the one at each border of two runs. A row of one
     // gets a warp for every 8 of the runs that share it on average.
-    const int64_t all = int64_t(a.B) * (a.cache.heads / side) * groups;
+    const int64_t all = int64_t(a.B) * (a.cache.heads * groups / side);
     const int split = int(std::min<int64_t>(blocks - 1, all));
     if (split == 0) return cudaSuccess;
     int warps = 1;
@@ -978,8 +978,9 @@ cudaError_t launch_heads(const AttentionArgs& a, int num_sms, cudaStream_t strea
 }  // namespace
 
 size_t paged_attention_workspace(int64_t, int q_heads, int heads, int head_dim) {
-    const size_t rows = size_t(unit_rows(q_heads / heads));
-    return size_t(2 * kMaxBlocks * heads_at_once(heads)) * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
+    const int group = q_heads / heads;
+    const size_t rows = size_t(unit_rows(group));
+    return size_t(2 * kMaxBlocks * heads_at_once(heads * ((group + kRows - 1) / kRows))) * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
