@@ -29,11 +29,11 @@
 // next one takes them in, up to 8 heads need half the products, and the values
 // come through ldmatrix.trans.
 //
-// Measured on GB300 (6.77 TB/s copy): 1.07 GB of keys and values at 6.5 TB/s (two
-// sequences of 131072 tokens), 6.3 (256 of up to 4096), 6.1 (8 bits); 394 MB at
-// 5.7. DRAM is 70% busy in 270 MB, the warps issue 27% of the time (45% with 8
-// bits, whose conversions take the ALU pipe to 43%). Runs cost 12 us beside the
-// reading: 4 to the first step's arrival, 3 as SMs differ in speed, 2 to leave
+// Measured on GB300 (6.77 TB/s copy): 1.07 GB of keys and values at 6.6 TB/s (two
+// sequences of 131072 tokens), 6.4 (256 of up to 4096), 6.4 (8 bits); 394 MB at
+// 5.8. DRAM is 74% busy in 270 MB, the warps issue 24% of the time (46% with 8
+// bits, whose conversions take the ALU pipe to 44%). Runs cost about 10 us beside
+// the reading: 4 to the first step's arrival, 2 as SMs differ in speed, 1 to leave
 // the last unit, 4 for the second kernel.
 #include "few_device.cuh"
 #include "moe_launch.h"
@@ -255,10 +255,9 @@ struct Tile {
     static constexpr int kPer = kWarp / kVecs;                // rows that a warp copies with one instruction
     static constexpr int kSide = kStep * kBytes;              // keys or values of a step
     static constexpr int kStage = 2 * kSide;
-    // Of an SM; the rings fill its shared memory, and the registers allow no more. 394 MB, 8 heads a
-    // key head: bfloat16 heads of 128 68.6 us with 2 blocks of 3 stages, 256 ragged sequences of it
-    // 171 us (3 blocks of 2 stages 179 us); 8-bit heads of 64 77.2 us with 3 blocks of 3 stages, 79.2
-    // with 4, 83.3 with 3 of 2.
+    // Of an SM; the rings fill its shared memory, and the registers allow no more. When these were
+    // chosen: 256 ragged sequences of bfloat16 heads of 128 172 us with 2 blocks of 3 stages, 179 with 3
+    // of 2; 394 MB of 8-bit heads of 64 77.2 us with 3 blocks of 3 stages, 79.2 with 4, 83.3 with 3 of 2.
     static constexpr int kBlocks = D == 256 ? (E4M3 ? 2 : 1) : D == 128 && (!E4M3 || NH == 2) ? 2 : 3;
     static constexpr int kStages = kBlocks < 3 || kStage == 4096 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;            // of a warp
