@@ -123,3 +123,63 @@ def test_values_of_very_different_size(dev):  # noqa: F811
         k[page, at % 16, 0, 0] = -(far[:n] * 57 + (far[:n] > 0) * 3).to(torch.bfloat16)
         v[page, at % 16, 0, 1] = torch.where(far[:n] > 1, 3e38, 1.0).to(torch.bfloat16)
     check(q, cache, k, v, table, torch.tensor(lengths, dtype=torch.int32, device=dev), scale=1.0)
+
+
+def test_keys_and_values_laid_out_differently(dev):  # noqa: F811
+    from memory_bound_moe_gb300 import KVCache
+    g = rng(dev, 8)
+    for P in (4, 32):
+        lengths = [333, 0, 64, 5]
+        table, pages = make_table(lengths, P, dev, g)
+        _, k, _ = make_cache(pages, P, 4, 128, "bf16", dev, g, "token")
+        _, _, v = make_cache(pages, P, 4, 128, "bf16", dev, g, "head")
+        q = torch.randn((4, 8, 128), generator=g, device=dev).to(torch.bfloat16)
+        n = torch.tensor(lengths, dtype=torch.int32, device=dev)
+        check(q, KVCache(k, v), k, v, table, n)
+        check(q, KVCache(k, v), k, v, widened(table, P, 200000), n)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv", [(1024, 8), (1024, 1024), (1023, 3)])
+def test_the_most_heads(dev, kind, Hq, Hkv):  # noqa: F811
+    g = rng(dev, Hkv)
+    lengths = [90, 1, 0]
+    table, pages = make_table(lengths, 16, dev, g)
+    cache, k, v = make_cache(pages, 16, Hkv, 64, kind, dev, g)
+    q = torch.randn((3, Hq, 64), generator=g, device=dev).to(torch.bfloat16)
+    check(q, cache, k, v, table, torch.tensor(lengths, dtype=torch.int32, device=dev))
+
+
+def test_a_million_tokens_and_many_sequences(dev):  # noqa: F811
+    g = rng(dev, 9)
+    for lengths, P, kind in (([1000003, 5], 1024, "e4m3"), ([1000003, 70000], 16, "bf16"), ([i % 4 for i in range(5000)], 2, "bf16")):
+        table, pages = make_table(lengths, P, dev, g)
+        cache, k, v = make_cache(pages, P, 1, 64, kind, dev, g)
+        q = (3 * torch.randn((len(lengths), 3, 64), generator=g, device=dev)).to(torch.bfloat16)
+        check(q, cache, k, v, table, torch.tensor(lengths, dtype=torch.int32, device=dev))
+
+
+def test_two_graphs_that_share_a_workspace(dev):  # noqa: F811
+    from memory_bound_moe_gb300 import moe_paged_attention, moe_paged_attention_workspace_size
+    g = rng(dev, 10)
+    ws = torch.empty(moe_paged_attention_workspace_size(9, 32, 4, 128), dtype=torch.uint8, device=dev)
+    made = []
+    for lengths, Hq, Hkv, wide in (([9000, 40, 3000], 32, 4, 200000), ([700] * 9, 16, 2, 0), ([20000], 8, 1, 0)):
+        table, pages = make_table(lengths, 16, dev, g)
+        table = widened(table, 16, wide) if wide else table
+        cache, k, v = make_cache(pages, 16, Hkv, 128, "bf16", dev, g)
+        q = torch.randn((len(lengths), Hq, 128), generator=g, device=dev).to(torch.bfloat16)
+        n = torch.tensor(lengths, dtype=torch.int32, device=dev)
+        want = check(q, cache, k, v, table, n, workspace=ws)
+        out = torch.empty_like(q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe_paged_attention(q, cache, table, n, workspace=ws, out=out)
+        made.append((graph, out, want, (cache, table, q, n)))   # a graph does not keep what it reads
+    for _ in range(20):
+        for graph, out, _, _ in made:
+            out.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _ in made:
+        assert torch.equal(out, want)
