@@ -243,7 +243,8 @@ __device__ __forceinline__ Cursor find_run(const AttentionArgs& a, int units, in
 }
 
 // ---------------------------------------------------------------------------
-// Main kernel: NH groups of 8 query heads
+// Main kernel: NH groups of 8 query heads. ranks = 0: this block's run of all
+// units; else clusters of `ranks` blocks, a unit each (side is then 1).
 // ---------------------------------------------------------------------------
 
 template <int D, bool E4M3, int NH>
@@ -339,7 +340,8 @@ __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
 }
 
 template <int D, bool E4M3, int NH>
-__global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks) attention_kernel(const AttentionArgs a, int groups, int side, int ranks) {
+__global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
+    attention_kernel(const AttentionArgs a, int groups, int side, int ranks) {
     using T = Tile<D, E4M3, NH>;
     constexpr int kD16 = D / 16, kStep = T::kStep, kTiles8 = kStep / 8, kStages = T::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -979,7 +981,8 @@ cudaError_t launch_heads(const AttentionArgs& a, int num_sms, cudaStream_t strea
 size_t paged_attention_workspace(int64_t, int q_heads, int heads, int head_dim) {
     const int group = q_heads / heads;
     const size_t rows = size_t(unit_rows(group));
-    return size_t(2 * kMaxBlocks * heads_at_once(heads * ((group + kRows - 1) / kRows))) * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
+    const size_t results = size_t(2 * kMaxBlocks * heads_at_once(heads * ((group + kRows - 1) / kRows)));
+    return results * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
