@@ -7,6 +7,9 @@
 //
 // lengths may be cached itself and free_count_out free_count itself: the
 // cluster meets once between the last read of these and the first write.
+//
+// GB300: 3.1 us for 16 requests with a token each, 6.5 us for 1023 with 32768
+// places: two dependent loads, two scans, a bisection per token and its stores.
 #include "few_device.cuh"
 #include "moe_launch.h"
 
