@@ -938,15 +938,15 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
 
     // Units that are few and cannot be long go to clusters of as many blocks as find room at once (with
     // an eighth to spare: clusters do not fit everywhere), each unit's tokens in equal shares: one kernel
-    // and no join, where the runs cost 4 to 7 us more but share uneven lengths evenly. GB300, bfloat16,
-    // D = 128, clusters against runs, in us: 8 units of 1000 tokens 7.5 / 11.9, of 4000 11.9 / 14.3, of
-    // 8000 19.8 / 17.9; 2 units of 2000 8.7 / 9.3, of 4000 11.8 / 9.5; 64 units of 1000 10.9 / 18.0, of 1
-    // to 8000 38.0 / 36.7; 256 units of 1000 27.7 / 32.4, of 1 to 4000 66.9 / 53.7. Hence at most 256 KB
-    // of keys per block, and fewer where few units leave most SMs idle.
+    // and no join, where the runs cost 2 to 5 us more but share uneven lengths evenly. GB300, bfloat16,
+    // D = 128, clusters against runs, in us: 8 units of 1000 tokens 7.4 / 9.4, of 4000 11.3 / 10.9, of
+    // 8000 18.2 / 17.4; 2 units of 2000 8.5 / 9.6, of 4000 11.2 / 9.8; 64 units of 1000 10.7 / 15.7, of 1
+    // to 4000 21.4 / 22.6, of 1 to 8000 35.1 / 32.0; 256 units of 1000 27.5 / 31.2, of 1 to 2000 35.3 /
+    // 32.3. Hence at most 256 KB of keys per block, and fewer where few units leave most SMs idle.
     const int64_t clusters = int64_t(a.B) * a.cache.heads * groups;
     int ranks = kMaxRanks;
     while (ranks > 0 && clusters * ranks * 8 > int64_t(num_sms) * cluster_occ * 7) ranks /= 2;
-    if (ranks > 0 && longest * T::kBytes <= ranks * std::min<int64_t>(262144, 65536 + 16384 * clusters))
+    if (ranks > 0 && longest * T::kBytes <= ranks * std::min<int64_t>(262144, 65536 + 8192 * clusters))
         return launch_cluster(kernel, dim3(unsigned(clusters * ranks)), dim3(kNt), ranks, T::kSmem + kShare, stream, a, groups, 1, ranks);
     const int side = heads_at_once(a.cache.heads * groups);
     // no more blocks than the most tiles that these tables can hold need
