@@ -153,7 +153,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b, int ts) {
     Span s;
     const int64_t most = int64_t(a.max_pages) << a.cache.page_shift;
-    s.len = int(min(int64_t(max(__ldg(a.lengths + b), 0)), most));
+    s.len = int(min(int64_t(max(a.lengths[b], 0)), most));
     s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
     s.tiles = s.len == 0 ? 0 : ((s.len - 1) >> ts) + 1 - (s.first >> ts);
     return s;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
             next_t0 = ahead_from + (ahead_j++ * phases + phase) * kStep;
             const int t = next_t0 + lane % kStep;
             if (t >= ahead.s.first && t < ahead.s.len) {
-                const int pg = __ldg(a.block_table + int64_t(ahead.b) * a.max_pages + (t >> a.cache.page_shift));
+                const int pg = a.block_table[int64_t(ahead.b) * a.max_pages + (t >> a.cache.page_shift)];
                 next_page = pg < a.cache.num_pages ? pg : -1;
             }
         }

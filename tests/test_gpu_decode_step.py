@@ -163,3 +163,36 @@ def test_prompts_in_chunks_then_tokens(dev):  # noqa: F811
     moe.moe_page_release(s.finished, s.table, s.lengths, s.free, s.count, P)
     assert int(s.count) == count + used[1] + used[3] + used[6]
     assert s.lengths.tolist() == [0 if f else n + 1 for n, f in zip(prompt, s.finished.tolist())]
+
+
+def test_tables_in_place_in_front_of_attention(dev):  # noqa: F811
+    """Lengths, table and stack updated in place and read at once by the next call: every step sees its own."""
+    import memory_bound_moe_gb300 as moe
+    g = rng(dev, 9)
+    many, page, steps = 1100, 1, 48
+    cache, k, v = make_cache(many * steps, page, 1, 64, "bf16", dev, g)
+    q = torch.randn((many, 2, 64), generator=g, device=dev).to(torch.bfloat16)
+    ws = torch.empty(moe.moe_paged_attention_workspace_size(many, 2, 1, 64), dtype=torch.uint8, device=dev)
+    i32 = dict(dtype=torch.int32, device=dev)
+    added, order = torch.ones(many, **i32), torch.randperm(many * steps, generator=g, device=dev).int()
+
+    def run(wait):
+        lengths, table, count = torch.zeros(many, **i32), torch.zeros((many, steps), **i32), torch.tensor([many * steps], **i32)
+        out = moe.PageTable(lengths, torch.empty(many + 1, **i32), torch.empty(8192, **i32),
+                            torch.empty(8192, dtype=torch.int64, device=dev), count, torch.empty(1, **i32))
+        results = torch.empty((steps, many, 2, 64), dtype=torch.bfloat16, device=dev)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            moe.moe_page_table(lengths, added, table, order, count, page, 8192, out=out)
+            if wait:
+                torch.cuda.synchronize()
+            moe.moe_paged_attention(q, cache, table, lengths, workspace=ws, out=results[i])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return results
+
+    want = run(True)
+    assert not torch.equal(want[0], want[1]) and want.isfinite().all()
+    for _ in range(10):
+        assert torch.equal(run(False), want)
