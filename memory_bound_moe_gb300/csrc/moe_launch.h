@@ -188,6 +188,7 @@ struct AttentionArgs {
     int64_t q_stride;            // elements
     int B, q_heads, max_pages, window;
     float scale;
+    float score, score_up;       // set by the launch: their product is scale * k_scale * log2 e
 };
 size_t paged_attention_workspace(int64_t B, int q_heads, int heads, int head_dim);
 cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream);

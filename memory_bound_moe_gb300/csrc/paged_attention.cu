@@ -38,6 +38,9 @@
 #include "few_device.cuh"
 #include "moe_launch.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace moe {
 namespace {
 
@@ -50,7 +53,8 @@ constexpr int kMinTiles = 3;         // tiles of a run, at least
 // (GB300, the decode batch of 16 sequences of 1 to 8192 tokens: 53.9 us at 0, 52.4 at 1, 52.2 at 2).
 constexpr int kUnitCost = 2;
 static_assert(kMinTiles > kUnitCost, "a run goes on");
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr double kLog2e = 1.44269504088896340736;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 // ---------------------------------------------------------------------------
 // Workspace: for every run two partial results (a unit that began in an earlier
@@ -139,6 +143,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
     uint32_t d;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(w));
     return d;
+}
+
+// The means of four columns' values into the output. The values' scale comes after the division by the
+// weights' sum: the sum is up to 2^45, and a scale near 2^-126 divided by it would be 0.
+__device__ __forceinline__ uint2 pack_out(const float4& y, float v_scale) {
+    return make_uint2(pack_bf16x2(y.x * v_scale, y.y * v_scale), pack_bf16x2(y.z * v_scale, y.w * v_scale));
 }
 
 // ---------------------------------------------------------------------------
@@ -468,10 +478,10 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
         const int at = c.unit * side + mine_head, chunk = at % groups;
         const int rows = min(kRows, group - chunk * kRows), h0 = at / groups * group + chunk * kRows;
 
-        float f_row[NH];   // what a row's scores are multiplied by, with log2 e
+        float f_row[NH];   // what a row's scores are multiplied by, with log2 e; and then by score_up
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            f_row[h] = a.scale * a.cache.k_scale * kLog2e;
+            f_row[h] = a.score;
             if constexpr (E4M3) {
                 float most = 0.0f;
 #pragma unroll
@@ -547,7 +557,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
 #pragma unroll
                 for (int n = 0; n < kTiles8; ++n)
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) x[n][2 * h + z] *= f_row[h];
+                    for (int z = 0; z < 2; ++z) x[n][2 * h + z] = x[n][2 * h + z] * f_row[h] * a.score_up;
             }
             if (mask != kAll) {
                 const uint32_t seen = mask >> (quad * 2);
@@ -671,8 +681,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
             if (ranks > 0)
                 *reinterpret_cast<float4*>(s_co + r * D + d) = y;
             else if (whole)
-                *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) =
-                    make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+                *reinterpret_cast<uint2*>(a.out + (int64_t(c.b) * a.q_heads + h0 + r) * D + d) = pack_out(y, a.cache.v_scale);
             else
                 *reinterpret_cast<float4*>(ws.o + (slot * unit_rows(group) + r) * D + d) = y;
         };
@@ -694,7 +703,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
 #pragma unroll
                 for (int h = 0; h < kHalf; ++h) {
                     const float sum = l[h0r + h];
-                    f[h] = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+                    f[h] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
                     if (quad == 0 && g + 8 * (h0r + h) < rows) store_sum(g + 8 * (h0r + h), m[h0r + h], sum);
                 }
                 __syncwarp();
@@ -724,7 +733,7 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
                     for (int w = mine_head; w < kWarps; w += side) most = fmaxf(most, s_m[w][r]);
                     const float base = most == -INFINITY ? 0.0f : most;
                     for (int w = mine_head; w < kWarps; w += side) sum += ex2_approx(s_m[w][r] - base) * s_l[w][r];
-                    const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
+                    const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
                     for (int w = mine_head; w < kWarps; w += side) s_f[w][r] = ex2_approx(s_m[w][r] - base) * inv;
                     if (ranks > 0) {
                         s_cm[r] = most;
@@ -797,8 +806,8 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
                 y.w += f * z[k].w;
             }
         const int64_t row = int64_t(u / units) * a.q_heads + head * group + chunk * kRows + r;
-        const float f = sum == 0.0f ? 0.0f : a.cache.v_scale / sum;
-        *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+        *reinterpret_cast<uint2*>(a.out + row * D + d) = pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f), a.cache.v_scale);
         if (a.lse != nullptr && d == 0) a.lse[row] = (most + log2f(sum) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
     }
     cluster_sync();   // the others may still read this block's share
@@ -911,12 +920,12 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const Attention
     }
     if (!valid || sub != 0) return;
     const int64_t row = int64_t(n.b) * a.q_heads + head * group + chunk * kRows + r;
-    const float f = l == 0.0f ? 0.0f : a.cache.v_scale / l;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
     if (lane < kLanes)
 #pragma unroll
         for (int v = 0; v < kVecs; ++v)
             *reinterpret_cast<uint2*>(a.out + row * D + (lane + v * kLanes) * 4) =
-                make_uint2(pack_bf16x2(y[v].x * f, y[v].y * f), pack_bf16x2(y[v].z * f, y[v].w * f));
+                pack_out(make_float4(y[v].x * f, y[v].y * f, y[v].z * f, y[v].w * f), a.cache.v_scale);
     if (a.lse != nullptr && lane == 0) a.lse[row] = (m + log2f(l) - (E4M3 ? 15.0f : 0.0f)) * kLn2;
 }
 
@@ -985,7 +994,16 @@ size_t paged_attention_workspace(int64_t, int q_heads, int heads, int head_dim) 
     return results * (rows * head_dim + 2 * kRows) * sizeof(float) + kMaxBlocks * sizeof(Note);
 }
 
-cudaError_t launch_paged_attention(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const AttentionArgs& args, int num_sms, cudaStream_t stream) {
+    // scale k_scale log2 e may lie far outside float32 where the scores do not, so a power of two of it
+    // is a factor of its own. The other stays within 2^-100 .. 2^14 (but for products below 2^-226): with
+    // the 2^-126 .. 2^113 of a row of q (E4M3) it is in range, or so small that its scores are 0.
+    AttentionArgs a = args;
+    int e = 0;
+    const double f = frexp(double(a.scale) * double(a.cache.k_scale) * kLog2e, &e);
+    const int up = std::max(-126, std::min(127, e > 14 ? e - 14 : e < -100 ? e + 100 : 0));
+    a.score = float(ldexp(f, e - up));
+    a.score_up = float(ldexp(1.0, up));
     switch (a.cache.head_dim) {
         case 64: return launch_heads<64>(a, num_sms, stream);
         case 128: return launch_heads<128>(a, num_sms, stream);
