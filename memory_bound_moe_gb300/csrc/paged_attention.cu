@@ -145,6 +145,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
     return d;
 }
 
+// |x|, or 0 for an infinity or NaN.
+__device__ __forceinline__ float finite_size(float x) {
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.0f;
+}
+
 // The means of four columns' values into the output. The values' scale comes after the division by the
 // weights' sum: the sum is up to 2^45, and a scale near 2^-126 divided by it would be 0.
 __device__ __forceinline__ uint2 pack_out(const float4& y, float v_scale) {
@@ -487,11 +493,11 @@ __global__ void __launch_bounds__(kNt, Tile<D, E4M3, NH>::kBlocks)
 #pragma unroll
                 for (int k = 0; k < kD16; ++k)
 #pragma unroll
-                    for (int z = h; z < 4; z += 2) most = fmaxf(most, fmaxf(fabsf(bf16_lo(aq[k][z])), fabsf(bf16_hi(aq[k][z]))));
+                    for (int z = h; z < 4; z += 2) most = fmaxf(most, fmaxf(finite_size(bf16_lo(aq[k][z])), finite_size(bf16_hi(aq[k][z]))));
                 most = fmaxf(most, __shfl_xor_sync(kFull, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(kFull, most, 2));
-                // f16 holds q times 2^(14 - e), e the exponent of the row's largest (1 for a row of zeros or with an infinity)
-                const int e = most > 0.0f && most < INFINITY ? max(int(__float_as_uint(most) >> 23) - 127, -112) : 14;
+                // f16 holds q times 2^(14 - e), e the exponent of the row's largest finite value (14 for a row without one)
+                const int e = most > 0.0f ? max(int(__float_as_uint(most) >> 23) - 127, -112) : 14;
                 const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
                 f_row[h] *= __uint_as_float(uint32_t(127 - 14 + e) << 23);
 #pragma unroll
