@@ -617,8 +617,9 @@ moe_status_t moe_kv_append(const moe_bf16_t* q, int64_t q_stride, const moe_bf16
  * seen if lengths counts it (as after moe_page_table and moe_kv_append).
  * Scores, the softmax and all sums are float32. With a bfloat16 cache the
  * weights exp(..) enter the products as two bfloat16 terms (16 bits); with an
- * E4M3 cache as f16 (11 bits), and q as f16 times a power of two per row
- * (exact down to 2^-31 of the row's largest).
+ * E4M3 cache as two f16 terms (22 bits, or 2^-40 of the row's largest weight),
+ * and q as f16 times a power of two per row (exact down to 2^-31 of the row's
+ * largest).
  *
  * q [B, num_q_heads, head_dim] with tokens q_stride elements apart (as above),
  * out [B, num_q_heads, head_dim] dense, bfloat16, 16-byte aligned; lse [B,
