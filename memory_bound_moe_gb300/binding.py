@@ -796,8 +796,10 @@ class KVCache:
     head_dim], bfloat16, or float8_e4m3fn that stands for E4M3 times
     ``k_scale`` / ``v_scale``. Any strides with dense heads' rows will do (a
     transposed view of [pages, heads, page_size, head_dim], views of one array
-    that holds both). The tensors are checked here, once, and kept: the calls
-    that take the cache read and write them."""
+    that holds both). Types, sizes, strides, alignment and scales are checked
+    here, once, and the tensors are kept: the calls that take the cache read and
+    write them. A KVCache does not change: its attributes cannot be set, and a
+    call refuses it once ``k`` or ``v`` has been given other memory."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
         for name, t in (("k", k), ("v", v)):
@@ -818,11 +820,27 @@ class KVCache:
         strides = [s if n > 1 else 0 for t in (k, v) for s, n in zip(t.stride()[:3], t.shape[:3])]
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, int(k.dtype == torch.float8_e4m3fn), *strides,
                                     self.k_scale, self.v_scale)
+        # these keep the memory that the struct points at, whatever becomes of k and v, so that no other
+        # tensor can come to lie there
+        self._memory = (k.detach(), v.detach())
+        self._at = (k.data_ptr(), v.data_ptr())
+        # a call without sequences: the library's own checks of a cache
+        st = load_library().moe_paged_attention(None, 0, 0, self.heads, ctypes.addressof(self._struct), None, 1, None, 0, 1.0, None,
+                                                None, None, 0, None)
+        if st:
+            raise MoeError("KVCache", st)
         self._ptr = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):
+        if "_ptr" in self.__dict__:
+            raise AttributeError(f"{name} of a KVCache cannot be changed: make another")
+        super().__setattr__(name, value)
 
     def _on(self, dev: int) -> int:
         if self.device_index != dev:
             raise ValueError(f"the cache is on cuda:{self.device_index}, expected cuda:{dev}")
+        if (self.k.data_ptr(), self.v.data_ptr()) != self._at:
+            raise ValueError("the cache's k or v has been given other memory: make another KVCache")
         return self._ptr
 
 
