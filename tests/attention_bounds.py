@@ -15,14 +15,15 @@ U32 = 2.0 ** -23
 JOINED = 96     # partial results that a sum may pass through: those of 640 runs over eight warps, and these
 
 
-def chain(lengths, Hkv, G, D, sms):
-    """Tokens of a sequence that one warp adds up, at most. Either a block of a cluster has up to 256 KB of
-    keys (4096 tokens at 64 bytes, a quarter of them for each warp), or all heads' tokens and a few tiles
-    (of at most 128 tokens) for each unit are shared evenly by a block per SM or more, whose four warps
-    have each a head, or a quarter of the tokens."""
-    groups = -(-G // 16)
-    units = Hkv * groups / 4
-    return max(1024, math.ceil(sum(units * (n + 512) for n in lengths) / sms) + 512)
+def chain(lengths, Hkv, G, row_bytes, sms):
+    """Tokens of a sequence that one warp adds up, at most. Short ones (up to 2 MB of one head's keys) may go to
+    clusters, where a block has at most 256 KB of them and each of its four warps a quarter; else all heads'
+    tokens, and a few tiles of at most 128 tokens for each unit, are shared evenly by a block per SM or more,
+    whose warps have each a head, or a quarter of the tokens."""
+    units = Hkv * -(-G // 16) / 4
+    runs = math.ceil(sum(units * (n + 512) for n in lengths) / sms) + 128
+    longest = max(lengths)
+    return max(runs, min(longest, 262144 // row_bytes) // 4 + 128 if longest * row_bytes <= 8 * 262144 else 0)
 
 
 def attention(q, k_cache, v_cache, table, lengths, scale, chain, window=0, k_scale=1.0, v_scale=1.0, without=(), joined=JOINED):
@@ -59,11 +60,47 @@ def attention(q, k_cache, v_cache, table, lengths, scale, chain, window=0, k_sca
             dx = size * (D + 16) * U32
             # a weight: the exponential and its rounding, with an 8-bit cache to 2^-22, or 2^-40 of the
             # largest, else to 2^-16
-            dw = torch.expm1(2 * dx) + 2.0 ** -21 + (2.0 ** -22 if e4m3 else 2.0 ** -16) + sums
+            dw = torch.expm1(2 * dx) + 2.0 ** -21 + (2.0 ** -22 if e4m3 else 2.0 ** -16)
             small = (2.0 ** -40 * v.abs().sum(0) / total * v_scale) if e4m3 else 0.0
             heads = slice(h * G, (h + 1) * G)
             out[b, heads], lse[b, heads] = y, (m + torch.log(total))[:, 0]
-            tol[b, heads] = 2.0 ** -8 * y.abs() + 2 * dw * mass + small + 2.0 ** -133
+            tol[b, heads] = 2.0 ** -8 * y.abs() + (2 * dw + sums) * mass + sums * y.abs() + small + 2.0 ** -133
             # the largest score and the sum's logarithm are float32 in units of ln 2; with an 8-bit cache 15 apart
             ltol[b, heads] = (2 * dx + 2.0 ** -21 + sums + 2.0 ** -22 * (m.abs() + torch.log(total) + 24))[:, 0]
     return out, lse, tol, ltol
+
+
+# Sequences whose scores are all 0, so that the output counts tokens: the value of a token is 1 in one column, 0 in
+# the others. A sequence is cut into equal blocks, a column (of one of several passes) each; a block holds at most
+# 1024 tokens, so that 16 tokens left out or taken twice are more than a bfloat16's rounding.
+
+COUNTED = 1024
+
+
+def passes(n, D):
+    return max(1, -(-n // (COUNTED * D)))
+
+
+def column(n, D, count, r, head, device):
+    """For each of n tokens the column that it counts in during pass r of `count`, or -1."""
+    block = torch.arange(n, device=device) * (D * count) // max(1, n)
+    return torch.where(block // D == r, (block % D + 7 * head) % D, -1)
+
+
+def counted(cols, D, times=None):
+    """The tokens that each column counts; `times`: how often each token is taken (default once)."""
+    there = cols >= 0
+    w = torch.ones(cols.shape, dtype=torch.float64, device=cols.device) if times is None else times.double()
+    return torch.zeros(D, dtype=torch.float64, device=cols.device).index_add_(0, cols[there], w[there])
+
+
+def counted_tol(mean, chain, e4m3):
+    """Bound of the error of a column's mean. The weights are 1 (2^15 with an 8-bit cache, to 2^-22), and the second
+    bfloat16 term at most adds 2^-20."""
+    return (2.0 ** -8 + 2.0 ** -20 + (2 * (chain + JOINED) * U32 + 2.0 ** -21 if e4m3 else 0.0)) * mean
+
+
+def counted_lse_tol(n, chain, e4m3):
+    """Bound of the error of ln n: the sum of the ones is exact, with an 8-bit cache a lane adds up a quarter of
+    what its warp does, rounded to nearest."""
+    return 2.0 ** -22 * (math.log(n) + 24) + (((chain / 4 + JOINED) * 2.0 ** -24 + 2.0 ** -22) if e4m3 else 0.0)
