@@ -584,8 +584,8 @@ moe_status_t moe_page_release(const int32_t* finished, int64_t B, int page_size,
  *   +-448 (NaN stays NaN). Slot s is token s % page_size of page s / page_size.
  *
  * Tokens whose slot lies outside [0, num_pages * page_size), or with a
- * position outside [0, max_positions), are left out: their rows of q_out and
- * k_out and the cache keep what they held. Slots of the other tokens must
+ * position outside [0, max_positions), are left out (refused requests' and
+ * padding): their rows of q_out and k_out and the cache keep what they held. Slots of the other tokens must
  * differ (of two equal ones either is stored, element by element).
  * q, q_out [N, num_q_heads, head_dim], k, k_out, v [N, num_heads, head_dim]:
  * bfloat16, 16-byte aligned, the rows of a token dense and tokens `*_stride`
@@ -613,9 +613,17 @@ moe_status_t moe_kv_append(const moe_bf16_t* q, int64_t q_stride, const moe_bf16
  *   out[b, h] = bf16_rn( sum_j exp(x_j - m) value(j) / sum_j exp(x_j - m) ),  m = max x_j
  *   lse[b, h] = m + ln sum_j exp(x_j - m)
  * An empty J_b, or scores of -infinity alone, give out = 0 and lse = -infinity;
- * other scores that are not finite make their row's results NaN. The new token's own key is
+ * scores of +infinity or NaN make their row's results NaN. The new token's own key is
  * seen if lengths counts it (as after moe_page_table and moe_kv_append).
- * Scores, the softmax and all sums are float32. With a bfloat16 cache the
+ * Row b of q belongs to row b of block_table. The rows of moe_page_table and
+ * moe_kv_append are by token: request b's are starts[b] .. starts[b + 1] - 1.
+ * They are the attention's rows as they are only if every request brings exactly
+ * one token; else the caller takes q's row starts[b + 1] - 1 of each request
+ * (of a refused one it may lie behind the last row: any other will do), and a
+ * length of 0 for those without a token.
+ * Scores, the softmax and all sums are float32, and infinite where they pass its
+ * range; a weight below 2^-126 of the row's largest counts as 0 (which makes an
+ * infinite value NaN). With a bfloat16 cache the
  * weights exp(..) enter the products as two bfloat16 terms (16 bits); with an
  * E4M3 cache as two f16 terms (22 bits, or 2^-40 of the row's largest weight),
  * and q as f16 times a power of two per row (exact down to 2^-31 of the row's

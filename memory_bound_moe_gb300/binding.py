@@ -930,9 +930,10 @@ def moe_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, p
     head_dim]`` by ``cos_sin [max_positions, rot]`` (float32, cosines then
     sines; None: no rotation) at ``positions`` (int32 [N]), and the write of
     k and ``v`` into ``cache`` at ``slots`` (int64 [N]; a token with a slot
-    outside the cache is left out, its rows of ``q_out`` and ``k_out`` too). q,
-    k and v (bfloat16) may be slices of one projection. Returns ``q_out`` (new
-    when omitted; q itself for in place); the rotated k goes to ``k_out`` too
+    outside the cache is left out, its rows of ``q_out`` and ``k_out`` keep what
+    they held). q, k and v (bfloat16) may be slices of one projection. Returns
+    ``q_out`` (q itself for in place; new when omitted, and then undefined in
+    the rows of tokens that are left out); the rotated k goes to ``k_out`` too
     when one is given. ``q`` may be None."""
     if k.dim() != 3 or (q is not None and q.dim() != 3) or (cos_sin is not None and cos_sin.dim() != 2):
         raise ValueError("q must be [N, num_q_heads, head_dim], k [N, heads, head_dim] and cos_sin [max_positions, rot]")
@@ -977,7 +978,10 @@ def moe_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tens
     """Attention of one token per sequence, ``q [B, num_q_heads, head_dim]``
     (bfloat16), over the first ``lengths[b]`` (int32) cached tokens in the
     pages ``block_table[b]`` (int32 [B, max_pages]), or the last ``window`` of
-    them. ``scale`` defaults to head_dim^-0.5. Returns ``out`` [B, num_q_heads,
+    them. Row b of q is sequence b's: a step's rows, which are by token, serve
+    as they are only if every request brought one token (else
+    ``q[(step.starts[1:] - 1).clamp(0, len(q) - 1).long()]``, and a length of 0
+    for a request without any). ``scale`` defaults to head_dim^-0.5. Returns ``out`` [B, num_q_heads,
     head_dim]; ``lse`` (float32 [B, num_q_heads]), when given, gets the
     logarithms of the softmax sums. ``workspace``: a uint8 tensor of
     ``moe_paged_attention_workspace_size(B, num_q_heads, heads, head_dim)``
