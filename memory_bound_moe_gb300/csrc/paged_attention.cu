@@ -959,17 +959,27 @@ cudaError_t launch_d(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
     const int group = a.q_heads / a.cache.heads, groups = (group + kRows - 1) / kRows;
     const int64_t table = int64_t(a.max_pages) << a.cache.page_shift, longest = a.window > 0 ? std::min<int64_t>(table, a.window) : table;
 
-    // Units that are few and cannot be long go to clusters of as many blocks as find room at once (with
-    // an eighth to spare: clusters do not fit everywhere), each unit's tokens in equal shares: one kernel
-    // and no join, where the runs cost 2 to 5 us more but share uneven lengths evenly. GB300, bfloat16,
-    // D = 128, clusters against runs, in us: 8 units of 1000 tokens 7.4 / 9.4, of 4000 11.3 / 10.9, of
-    // 8000 18.2 / 17.4; 2 units of 2000 8.5 / 9.6, of 4000 11.2 / 9.8; 64 units of 1000 10.7 / 15.7, of 1
-    // to 4000 21.4 / 22.6, of 1 to 8000 35.1 / 32.0; 256 units of 1000 27.5 / 31.2, of 1 to 2000 35.3 /
-    // 32.3. Hence at most 256 KB of keys per block, and fewer where few units leave most SMs idle.
-    const int64_t clusters = int64_t(a.B) * a.cache.heads * groups;
+    // Units that are few and cannot be long go to clusters of as many blocks as find room at once (heads
+    // of 256 in bfloat16: 15 of 8 blocks, not the 19 that SMs / 8 would give), each unit's tokens in equal
+    // shares: one kernel and no join. The runs cost 2 to 3 us more, but share all tokens over all blocks,
+    // however many units there are and however unlike. What a cluster's block has beyond its share in that
+    // (units taken to be 3/4 of the longest on average) may be as many tokens as are read in those 2.5 us;
+    // a block is bound by its warps, so that is a number of tokens of a head size and type, not of bytes.
+    // GB300, us, clusters / runs: bfloat16 D = 128, 2 units of 2048 tokens 8.8 / 10.3, of 4096 12.6 / 10.5; 8
+    // of 2000 9.4 / 10.5, of 4000 13.0 / 12.4; 64 of 4096 28.6 / 31.9, of 1 to 4096 21.9 / 21.9; D = 64, 8 of
+    // 4096 10.1 / 10.4, of 8192 14.8 / 11.5; D = 256, 8 of 2048 12.7 / 14.2, 48 windows of 1023 18.5 / 21.5.
+    // 8 bits, D = 64, 64 of 1024 9.6 / 11.3, of 1 to 8192 24.0 / 18.3; D = 128, 8 of 2048 9.5 / 11.6, of 8192
+    // 18.1 / 14.5, 64 of 1 to 8192 32.9 / 25.2; D = 256, 16 of 2048 14.5 / 15.6, 64 of 1 to 4096 31.0 / 26.5.
+    // In 490 such calls of 2 to 256 units the way taken was 13% slower than the other at most.
+    static ClusterSlots cluster_slots;
+    uint32_t slots[kMaxRanks + 1];
+    err = cluster_slots.get(kernel, kNt, T::kSmem + kShare, num_sms * cluster_occ, slots);
+    if (err != cudaSuccess) return err;
+    const int64_t clusters = int64_t(a.B) * a.cache.heads * groups, everywhere = int64_t(num_sms) * occ;
+    constexpr int64_t kAhead = D == 64 ? 520 : D == 256 ? 310 : E4M3 ? 480 : 400;
     int ranks = kMaxRanks;
-    while (ranks > 0 && clusters * ranks * 8 > int64_t(num_sms) * cluster_occ * 7) ranks /= 2;
-    if (ranks > 0 && longest * T::kBytes <= ranks * std::min<int64_t>(262144, 65536 + 8192 * clusters))
+    while (ranks > 0 && clusters > slots[ranks]) ranks /= 2;
+    if (ranks > 0 && longest * (4 * everywhere - 3 * clusters * ranks) <= 4 * kAhead * everywhere * ranks)
         return launch_cluster(kernel, dim3(unsigned(clusters * ranks)), dim3(kNt), ranks, T::kSmem + kShare, stream, a, groups, 1, ranks);
     const int side = heads_at_once(a.cache.heads * groups);
     // no more blocks than the most tiles that these tables can hold need

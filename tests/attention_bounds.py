@@ -15,15 +15,15 @@ U32 = 2.0 ** -23
 JOINED = 96     # partial results that a sum may pass through: those of 640 runs over eight warps, and these
 
 
-def chain(lengths, Hkv, G, row_bytes, sms):
-    """Tokens of a sequence that one warp adds up, at most. Short ones (up to 2 MB of one head's keys) may go to
-    clusters, where a block has at most 256 KB of them and each of its four warps a quarter; else all heads'
-    tokens, and a few tiles of at most 128 tokens for each unit, are shared evenly by a block per SM or more,
-    whose warps have each a head, or a quarter of the tokens."""
+def chain(lengths, Hkv, G, sms):
+    """Tokens of a sequence that one warp adds up, at most. Short ones (up to 16640 tokens) may go to clusters of up
+    to 8 blocks, whose four warps share up to 2080 tokens; else all heads' tokens, and a few tiles of at most 128
+    tokens for each unit, are shared evenly by a block per SM or more, whose warps have each a head, or a quarter
+    of the tokens."""
     units = Hkv * -(-G // 16) / 4
     runs = math.ceil(sum(units * (n + 512) for n in lengths) / sms) + 128
     longest = max(lengths)
-    return max(runs, min(longest, 262144 // row_bytes) // 4 + 128 if longest * row_bytes <= 8 * 262144 else 0)
+    return max(runs, min(longest, 2080) // 4 + 128 if longest <= 8 * 2080 else 0)
 
 
 def attention(q, k_cache, v_cache, table, lengths, scale, chain, window=0, k_scale=1.0, v_scale=1.0, without=(), joined=JOINED):

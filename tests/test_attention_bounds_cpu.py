@@ -17,7 +17,7 @@ def test_random_sequences_show_a_lost_tile(kind, n, D, lost):
     q = (0.1 * torch.randn((1, 4, D), generator=g)).to(torch.bfloat16)   # scores well below 1: their errors count little
     k, v = (torch.randn((-(-n // 16), 16, 1, D), generator=g).to(dt) for _ in "kv")
     table = torch.arange(k.shape[0], dtype=torch.int32)[None]
-    chain = bounds.chain([n], 1, 4, D * k.element_size(), SMS)
+    chain = bounds.chain([n], 1, 4, SMS)
     call = lambda **kw: bounds.attention(q, k, v, table, [n], D ** -0.5, chain, **kw)   # noqa: E731
     want, want_lse, tol, ltol = call()
     assert (tol < 0.02 * v.float().abs().max()).all()
@@ -31,7 +31,7 @@ def test_random_sequences_show_a_lost_tile(kind, n, D, lost):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("n,D", [(1000003, 64), (1000003, 256), (131072, 64), (70001, 128), (40000, 128), (9000, 256), (777, 64)])
 def test_counted_sequences_show_16_tokens(e4m3, n, D):
-    chain = bounds.chain([n], 1, 4, D if e4m3 else 2 * D, SMS)
+    chain = bounds.chain([n], 1, 4, SMS)
     R = bounds.passes(n, D)
     for times in (0, 2):
         for first in (0, 16, n // 3, n - 16):

@@ -41,7 +41,7 @@ def test_every_token_counts_once(dev, kind, lengths, Hq, Hkv, D, P, wide):  # no
     cache, given = KVCache(k, v), widened(table, P, wide) if wide else table
     q = torch.zeros((len(lengths), Hq, D), dtype=torch.bfloat16, device=dev)
     n32 = torch.tensor(lengths, dtype=torch.int32, device=dev)
-    chain = bounds.chain(lengths, Hkv, Hq // Hkv, D * k.element_size(), sms())
+    chain = bounds.chain(lengths, Hkv, Hq // Hkv, sms())
     R = max(bounds.passes(n, D) for n in lengths)
     for r in range(R):
         v.view(torch.int16 if kind == "bf16" else torch.uint8).zero_()
@@ -85,7 +85,7 @@ def test_random_sequences(dev, kind, lengths, Hq, Hkv, D, P, window):  # noqa: F
     table, pages = make_table(lengths, P, dev, g)
     cache, k, v = make_cache(pages, P, Hkv, D, kind, dev, g)
     q = ((0.1 if kind == "bf16" else 0.1 / 0.84) * torch.randn((len(lengths), Hq, D), generator=g, device=dev)).to(torch.bfloat16)
-    chain = bounds.chain([min(n, window or n) for n in lengths], Hkv, Hq // Hkv, D * k.element_size(), sms())
+    chain = bounds.chain([min(n, window or n) for n in lengths], Hkv, Hq // Hkv, sms())
     f32 = lambda x: float(torch.tensor(x, dtype=torch.float32))   # noqa: E731
     want, want_lse, tol, ltol = bounds.attention(q, k, v, table, lengths, f32(D ** -0.5), chain, window, f32(cache.k_scale),
                                                  f32(cache.v_scale))
