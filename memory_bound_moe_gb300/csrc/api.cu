@@ -703,6 +703,8 @@ int log2_of(int64_t v) {
     return s;
 }
 
+static_assert(moe::kMaxRequests == MOE_MAX_REQUESTS, "the kernels' shared memory is for as many requests as the header allows");
+
 moe_status_t check_pages(int64_t B, int page_size, int max_pages) {
     if (B < 0 || page_size < 1 || max_pages < 1) return MOE_ERR_INVALID_ARG;
     if (!power_of_two(page_size) || page_size > MOE_KV_MAX_PAGE_SIZE) return MOE_ERR_UNSUPPORTED;

@@ -118,7 +118,7 @@ cudaError_t launch_layer_nvfp4(const LayerArgs& a, int num_sms, cudaStream_t str
 cudaError_t launch_layer_mxfp4(const LayerArgs& a, int num_sms, cudaStream_t stream);
 
 // Block tables and slot maps (page_table.cu). Sums over the requests are 64-bit.
-constexpr int kMaxRequests = 16384;   // MOE_MAX_REQUESTS
+constexpr int kMaxRequests = 16384;   // MOE_MAX_REQUESTS (checked in api.cu and page_table.cu)
 struct PageTableArgs {
     const int32_t* cached;       // may be lengths
     const int32_t* added;

@@ -43,6 +43,9 @@ __device__ __forceinline__ int64_t block_before(int64_t v, int64_t* s_sum, int64
     return (warp == 0 ? 0 : before) + x - v;
 }
 
+// 12 bytes of shared memory per request, and the warps' sums (a block may have 227 KB)
+static_assert(12 * kMaxRequests + kWarps * sizeof(int64_t) <= 227 * 1024, "all requests fit a block's shared memory");
+
 __device__ __forceinline__ int64_t at_least_zero(int32_t v) { return v > 0 ? v : 0; }
 
 __global__ void __launch_bounds__(kNt) page_table_kernel(const PageTableArgs a) {
