@@ -823,7 +823,8 @@ class KVCache:
         # these keep the memory that the struct points at, whatever becomes of k and v, so that no other
         # tensor can come to lie there
         self._memory = (k.detach(), v.detach())
-        self._at = (k.data_ptr(), v.data_ptr())
+        self._k_at, self._v_at = k.data_ptr(), v.data_ptr()
+        self._k_now, self._v_now = k.data_ptr, v.data_ptr   # bound: every call of the cache's operators asks
         # a call without sequences: the library's own checks of a cache
         st = load_library().moe_paged_attention(None, 0, 0, self.heads, ctypes.addressof(self._struct), None, 1, None, 0, 1.0, None,
                                                 None, None, 0, None)
@@ -839,7 +840,7 @@ class KVCache:
     def _on(self, dev: int) -> int:
         if self.device_index != dev:
             raise ValueError(f"the cache is on cuda:{self.device_index}, expected cuda:{dev}")
-        if (self.k.data_ptr(), self.v.data_ptr()) != self._at:
+        if self._k_now() != self._k_at or self._v_now() != self._v_at:
             raise ValueError("the cache's k or v has been given other memory: make another KVCache")
         return self._ptr
 
@@ -989,6 +990,7 @@ def moe_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tens
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [B, num_q_heads, head_dim] and block_table [B, max_pages]")
     B, nq, D = q.shape
+    max_pages = block_table.shape[1]
     dev = _device(q)
     ref = cache._on(dev)
     qp, qs = _token_rows(q, "q", (B, nq, cache.head_dim), dev)
@@ -998,7 +1000,7 @@ def moe_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tens
         workspace = _new((moe_paged_attention_workspace_size(B, nq, cache.heads, D),), _u8, q, stream)
     ws_bytes = workspace.numel()
     st = _lib_fast().moe_paged_attention(
-        qp, qs, B, nq, ref, _addr(block_table, "block_table", _i32, (B, block_table.shape[1]), dev), block_table.shape[1],
+        qp, qs, B, nq, ref, _addr(block_table, "block_table", _i32, (B, max_pages), dev), max_pages,
         _addr(lengths, "lengths", _i32, (B,), dev), window, D ** -0.5 if scale is None else scale,
         _addr(out, "out", _bf16, (B, nq, D), dev), _opt(lse, "lse", _f32, (B, nq), dev),
         _addr(workspace, "workspace", _u8, (ws_bytes,), dev), ws_bytes, _raw_stream(stream, dev))
