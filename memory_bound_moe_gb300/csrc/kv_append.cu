@@ -163,7 +163,7 @@ cudaError_t launch_d(const AppendArgs& a, int num_sms, cudaStream_t stream) {
     constexpr int kHeads = kWarp / (D / 16);
     const int rounds = (a.q_heads + 2 * a.cache.heads + kHeads - 1) / kHeads;   // of one warp, a head row each
     // a token's rounds on several warps where tokens alone leave SMs without: up to 16 or more warps
-    // an SM (1023 tokens of 16 + 2 heads of 256 into E4M3: 5.7 us; up to 32: 8.0 us)
+    // an SM (1023 tokens of 16 + 2 heads of 256 into E4M3: 5.4 us; up to 32: 8.0 us)
     int parts = 1;
     while (parts < rounds && int64_t(a.N) * parts < int64_t(num_sms) * 16) parts *= 2;
     parts = std::min(parts, rounds);

@@ -2,16 +2,16 @@
 //
 // The G = num_q_heads / num_heads query heads that share a key head make up to
 // 16 rows of an m16n8k16 product (more than 16: several groups), so a cached
-// element is read once for all of them and costs 4 G operations for 4 bytes: at
-// G = 16 that is 16 operations a byte, where this GPU has 280. Reading the
-// cache bounds it, and mma.sync keeps up with HBM at a quarter of its rate; a
-// 128-row tcgen05 tile would be empty to seven eighths or more.
+// element is read once for all of them and costs 4 G operations for 4 bytes (8
+// bits: 2): at G = 16 that is 16 (32) operations a byte, where this GPU has 280.
+// Reading the cache bounds it, and mma.sync keeps up with HBM at a quarter of its
+// rate (a third with 8 bits); a 128-row tcgen05 tile would be empty to seven
+// eighths or more.
 //
 // Split. A unit of work is (sequence, up to 4 key heads, or groups of 16 query
 // heads of one, side by side). All units' tiles, one after another, are cut into equal runs, one per
-// resident block: whatever the lengths are, every SM reads the same number of
-// bytes (the lengths are on the GPU, so every block adds them up for itself). A
-// unit inside one run is finished there; what a run has of a unit that goes on
+// resident block, whatever the lengths are (they are on the GPU, so every block adds them up for itself;
+// to enter a unit counts as two tiles, so a run of many short units reads less). A unit inside one run is finished there; what a run has of a unit that goes on
 // in another run goes to the workspace (at most two per run), and a second
 // kernel joins those in order of the runs. Units that are few and short go to a
 // cluster of blocks each instead, which joins them in its shared memory.
@@ -30,9 +30,9 @@
 // come through ldmatrix.trans.
 //
 // Measured on GB300 (6.77 TB/s copy): 1.07 GB of keys and values at 6.6 TB/s (two
-// sequences of 131072 tokens), 6.4 (256 of up to 4096), 6.4 (8 bits); 394 MB at
-// 5.8. DRAM is 74% busy in 270 MB, the warps issue 24% of the time (46% with 8
-// bits, whose conversions take the ALU pipe to 44%). Runs cost about 10 us beside
+// sequences of 131072 tokens), 6.4 (256 of up to 4096), 6.3 (8 bits); 269 MB at
+// 5.3. DRAM is 74% busy in 270 MB, the warps issue 25% of the time (48% with 8
+// bits, whose conversions take the ALU pipe to 45%). Runs cost about 11 us beside
 // the reading: 4 to the first step's arrival, 2 as SMs differ in speed, 1 to leave
 // the last unit, 4 for the second kernel.
 #include "few_device.cuh"
@@ -275,6 +275,9 @@ struct Tile {
     // Of an SM; the rings fill its shared memory, and the registers allow no more. When these were
     // chosen: 256 ragged sequences of bfloat16 heads of 128 172 us with 2 blocks of 3 stages, 179 with 3
     // of 2; 394 MB of 8-bit heads of 64 77.2 us with 3 blocks of 3 stages, 79.2 with 4, 83.3 with 3 of 2.
+    // D = 256 spills in three of its four kernels, 160 to 216 bytes a thread of 255 registers (8 bits with up
+    // to 8 heads fit): its output, q and a step's scores and weights are more than a thread may have. 8-bit
+    // heads of 128 with 9 to 16 query heads spill 12 bytes.
     static constexpr int kBlocks = D == 256 ? (E4M3 ? 2 : 1) : D == 128 && (!E4M3 || NH == 2) ? 2 : 3;
     static constexpr int kStages = kBlocks < 3 || kStage == 4096 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;            // of a warp
