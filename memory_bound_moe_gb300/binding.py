@@ -813,29 +813,27 @@ class KVCache:
                 raise ValueError("k and v must be CUDA tensors of one device")
             if t.stride(3) != 1:
                 raise ValueError(f"{name}: a head's row must be contiguous")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
-        self.num_pages, self.page_size, self.heads, self.head_dim = k.shape
-        self.device_index = k.get_device()
+        pages, page_size, heads, head_dim = k.shape
+        k_at, v_at = k.data_ptr(), v.data_ptr()
         # the stride of an axis of one entry says nothing
         strides = [s if n > 1 else 0 for t in (k, v) for s, n in zip(t.stride()[:3], t.shape[:3])]
-        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, int(k.dtype == torch.float8_e4m3fn), *strides,
-                                    self.k_scale, self.v_scale)
-        # these keep the memory that the struct points at, whatever becomes of k and v, so that no other
-        # tensor can come to lie there
-        self._memory = (k.detach(), v.detach())
-        self._k_at, self._v_at = k.data_ptr(), v.data_ptr()
-        self._k_now, self._v_now = k.data_ptr, v.data_ptr   # bound: every call of the cache's operators asks
+        struct = _CacheStruct(k_at, v_at, pages, page_size, heads, head_dim, int(k.dtype == torch.float8_e4m3fn), *strides,
+                              k_scale, v_scale)
+        ptr = ctypes.addressof(struct)
         # a call without sequences: the library's own checks of a cache
-        st = load_library().moe_paged_attention(None, 0, 0, self.heads, ctypes.addressof(self._struct), None, 1, None, 0, 1.0, None,
-                                                None, None, 0, None)
+        st = _lib_fast().moe_paged_attention(None, 0, 0, heads, ptr, None, 1, None, 0, 1.0, None, None, None, 0, None)
         if st:
             raise MoeError("KVCache", st)
-        self._ptr = ctypes.addressof(self._struct)
+        self.__dict__.update(
+            k=k, v=v, k_scale=float(k_scale), v_scale=float(v_scale), num_pages=pages, page_size=page_size, heads=heads,
+            head_dim=head_dim, device_index=k.get_device(), _struct=struct, _ptr=ptr,
+            # these keep the memory that the struct points at, whatever becomes of k and v, so that no other
+            # tensor can come to lie there
+            _memory=(k.detach(), v.detach()), _k_at=k_at, _v_at=v_at,
+            _k_now=k.data_ptr, _v_now=v.data_ptr)   # bound: every call of the cache's operators asks
 
     def __setattr__(self, name, value):
-        if "_ptr" in self.__dict__:
-            raise AttributeError(f"{name} of a KVCache cannot be changed: make another")
-        super().__setattr__(name, value)
+        raise AttributeError(f"{name} of a KVCache cannot be changed: make another")
 
     def _on(self, dev: int) -> int:
         if self.device_index != dev:
