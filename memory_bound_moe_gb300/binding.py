@@ -798,7 +798,7 @@ class KVCache:
     transposed view of [pages, heads, page_size, head_dim], views of one array
     that holds both). Types, sizes, strides, alignment and scales are checked
     here, once, and the tensors are kept: the calls that take the cache read and
-    write them. A KVCache does not change: its attributes cannot be set, and a
+    write them. A KVCache does not change: these attributes cannot be set, and a
     call refuses it once ``k`` or ``v`` has been given other memory."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
@@ -833,7 +833,9 @@ class KVCache:
             _k_now=k.data_ptr, _v_now=v.data_ptr)   # bound: every call of the cache's operators asks
 
     def __setattr__(self, name, value):
-        raise AttributeError(f"{name} of a KVCache cannot be changed: make another")
+        if name in self.__dict__:
+            raise AttributeError(f"{name} of a KVCache cannot be changed: make another")
+        super().__setattr__(name, value)
 
     def _on(self, dev: int) -> int:
         if self.device_index != dev:

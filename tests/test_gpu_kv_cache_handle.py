@@ -49,6 +49,16 @@ def test_attributes_cannot_be_set(dev):  # noqa: F811
             setattr(cache, name, value)
     assert cache.k is k and cache.v is v and (cache.k_scale, cache.v_scale) == (0.5, 0.25)
     assert (cache.num_pages, cache.page_size, cache.heads, cache.head_dim) == (4, 16, 2, 64)
+    cache.layer = 3     # a name of the caller's own
+
+    class Named(KVCache):
+        def __init__(self, name, *tensors):
+            self.name = name
+            super().__init__(*tensors)
+            self.used = 0
+
+    named = Named("first", k, v)
+    assert (named.name, named.used, cache.layer) == ("first", 0, 3)
 
 
 @pytest.mark.parametrize("side", ["k", "v"])
